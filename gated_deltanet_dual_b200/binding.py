@@ -28,7 +28,10 @@ EXPORTED = ("gdn_dual_forward", "gdn_dual_workspace_size", "gdn_dual_read_device
             "gdn_dual_noalloc_read_device_status", "gdn_dual_forward_test_wait_limit",
             "gdn_dual_read_device_status_where", "gdn_attn_forward_test_wait_limit",
             "gdn_dual_backward_conv", "gdn_dual_backward_conv_workspace_size",
-            "gdn_dual_forward_host", "gdn_dual_host_staging_size", "gdn_dual_host_read_device_status")
+            "gdn_dual_forward_host", "gdn_dual_host_staging_size", "gdn_dual_host_read_device_status",
+            "gdn_rotary_frequencies", "gdn_rotary_forward", "gdn_rotary_backward", "gdn_rotary_append",
+            "gdn_kv_extend", "gdn_prefix_attn", "gdn_prefix_attn_workspace_size")
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "ramp": 3}
 
 
 class GdnError(RuntimeError):
@@ -52,6 +55,39 @@ class AttnDesc(ctypes.Structure):
     """gdn_attn_desc of include/gdn_attention.h."""
     _fields_ = [(n, ctypes.c_int32) for n in ("num_docs", "num_heads", "num_kv_heads", "head_dim", "num_views",
                                                "block_size", "dtype", "reserved")]
+
+
+class RotaryDesc(ctypes.Structure):
+    """gdn_rotary_desc of include/gdn_rotary.h."""
+    _fields_ = ([(n, ctypes.c_int32) for n in ("num_rows", "num_positions", "num_heads", "num_kv_heads", "head_dim",
+                                                "rot_dim", "interleaved", "dtype")]
+                + [("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+                + [(n, ctypes.c_int64) for n in ("q_row_stride", "q_head_stride", "k_row_stride", "k_head_stride",
+                                                 "q_out_row_stride", "q_out_head_stride", "k_out_row_stride",
+                                                 "k_out_head_stride")])
+
+
+class AppendDesc(ctypes.Structure):
+    """gdn_append_desc of include/gdn_kvcache.h."""
+    _fields_ = ([(n, ctypes.c_int32) for n in ("num_rows", "num_heads", "num_kv_heads", "head_dim", "rot_dim",
+                                                "interleaved", "page_size", "num_pages", "dtype")]
+                + [("scale", ctypes.c_float)]
+                + [(n, ctypes.c_int64) for n in ("q_row_stride", "q_head_stride", "k_row_stride", "k_head_stride",
+                                                 "v_row_stride", "v_head_stride", "q_out_row_stride",
+                                                 "q_out_head_stride")])
+
+
+class KvExtendDesc(ctypes.Structure):
+    """gdn_kv_extend_desc of include/gdn_kvcache.h."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_seqs", "table_width", "page_size", "num_free", "max_new_tokens",
+                                               "prefix_len", "reserved0", "reserved1")]
+
+
+class PrefixAttnDesc(ctypes.Structure):
+    """gdn_prefix_attn_desc of include/gdn_kvcache.h."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_seqs", "num_tokens", "num_heads", "num_kv_heads", "head_dim",
+                                               "page_size", "num_pages", "table_width", "prefix_len", "causal",
+                                               "dtype")] + [("scale", ctypes.c_float)]
 
 
 _lock = threading.Lock()
@@ -104,6 +140,18 @@ def load_library(path: str = LIB_PATH):
                                                   ctypes.c_size_t, ctypes.c_int32, vp])
             lib.gdn_dual_host_read_device_status.restype = ctypes.c_int
             lib.gdn_dual_host_read_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int32), vp]
+            for name in ("gdn_rotary_frequencies", "gdn_rotary_forward", "gdn_rotary_backward", "gdn_rotary_append",
+                         "gdn_kv_extend", "gdn_prefix_attn"):
+                getattr(lib, name).restype = ctypes.c_int
+            dbl = ctypes.c_double
+            lib.gdn_rotary_frequencies.argtypes = [ctypes.c_int32, dbl, ctypes.c_int32, dbl, dbl, dbl, dbl, vp]
+            for name in ("gdn_rotary_forward", "gdn_rotary_backward"):
+                getattr(lib, name).argtypes = [ctypes.POINTER(RotaryDesc)] + [vp] * 7
+            lib.gdn_rotary_append.argtypes = [ctypes.POINTER(AppendDesc)] + [vp] * 11
+            lib.gdn_kv_extend.argtypes = [ctypes.POINTER(KvExtendDesc)] + [vp] * 12
+            lib.gdn_prefix_attn_workspace_size.restype = ctypes.c_size_t
+            lib.gdn_prefix_attn_workspace_size.argtypes = [ctypes.POINTER(PrefixAttnDesc)]
+            lib.gdn_prefix_attn.argtypes = [ctypes.POINTER(PrefixAttnDesc)] + [vp] * 8 + [ctypes.c_size_t, vp]
             _lib = lib
     return _lib
 
@@ -595,3 +643,282 @@ def backward_conv_workspace_size(desc: Desc, doc_offsets) -> int:
     fn.restype = ctypes.c_size_t
     fn.argtypes = [ctypes.POINTER(Desc), ctypes.POINTER(ctypes.c_int32)]
     return int(fn(ctypes.byref(desc), offs.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))))
+
+
+# ----------------------------------------------------------------------------- rotary positions
+class RotaryTable:
+    """The frequencies of a rotary embedding on the device (made by rotary_table, kept by the caller)."""
+
+    def __init__(self, turns: torch.Tensor, rot_dim: int, interleaved: bool, scale: float):
+        self.turns, self.rot_dim, self.interleaved, self.scale = turns, rot_dim, bool(interleaved), float(scale)
+
+
+def rotary_frequencies(rot_dim, *, base=10000.0, scaling="none", factor=1.0, original_len=0, beta_fast=32.0,
+                       beta_slow=1.0) -> np.ndarray:
+    """gdn_rotary_frequencies: the pairs' fractions of a turn per position, uint64 fixed point (host)."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling: {scaling!r} is none of {sorted(ROPE_SCALING)}")
+    turns = np.zeros(max(1, int(rot_dim) // 2), dtype=np.uint64)
+    st = load_library().gdn_rotary_frequencies(int(rot_dim), float(base), ROPE_SCALING[scaling], float(factor),
+                                               float(original_len), float(beta_fast), float(beta_slow), turns.ctypes.data)
+    if st != GDN_OK:
+        raise GdnError(st, f"gdn_rotary_frequencies failed: {status_string(st)}")
+    return turns[:int(rot_dim) // 2]
+
+
+def rotary_table(rot_dim, *, interleaved=False, base=10000.0, scaling="none", factor=1.0, original_len=0,
+                 beta_fast=32.0, beta_slow=1.0, attn_scale=None, device="cuda") -> RotaryTable:
+    """Frequencies of the first rot_dim elements of a head (scaling: "none", "linear", "ntk" or "ramp", as
+    include/gdn_rotary.h defines them).  attn_scale multiplies the rotated part; None means 1, and
+    0.1 ln(factor) + 1 for "ramp"."""
+    turns = rotary_frequencies(rot_dim, base=base, scaling=scaling, factor=factor, original_len=original_len,
+                               beta_fast=beta_fast, beta_slow=beta_slow)
+    if attn_scale is None:
+        attn_scale = 0.1 * float(np.log(factor)) + 1.0 if scaling == "ramp" else 1.0
+    return RotaryTable(torch.from_numpy(turns.view(np.int64).copy()).to(device), int(rot_dim), interleaved, attn_scale)
+
+
+def _i32(t: torch.Tensor, name: str, shape, device):
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        _check(t, name, shape, torch.int32, device)
+
+
+def _rows(t: Optional[torch.Tensor], name: str, shape, dtype, device):
+    """(row stride, head stride) in elements of [..., rows, heads, d] with contiguous heads."""
+    if t is None:
+        return 0, 0
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {shape}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype} != {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    st = t.stride()
+    if shape[-1] > 1 and st[-1] != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    if len(shape) == 4 and shape[0] > 1 and st[0] != shape[1] * st[1]:
+        raise ValueError(f"{name}: the views must lie {shape[1]} rows apart")
+    return st[-3], st[-2]
+
+
+class _On:
+    """Runs a call on the tensors' device: its current stream unless one is given.  Tensors that the call
+    allocated itself are kept alive for a stream other than the current one."""
+
+    def __init__(self, device, stream):
+        self.device, self.given = device, stream
+        self.guard = None
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        self.stream = torch.cuda.current_stream(self.device).cuda_stream if self.given is None else self.given
+        return self
+
+    def keep(self, *tensors):
+        if self.given is not None:
+            other = torch.cuda.ExternalStream(self.given, device=self.device)
+            for t in tensors:
+                t.record_stream(other)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _rotary(name, q, k, positions, table, q_out, k_out, stream):
+    lead = q if q is not None else k
+    if lead is None:
+        raise ValueError("q and k are both None")
+    dev, io = lead.device, lead.dtype
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if lead.ndim not in (3, 4):
+        raise ValueError("q and k must be [T, H, d] or [V, T, H, d]")
+    front, d = tuple(lead.shape[:-2]), lead.shape[-1]
+    T = front[-1]
+    H = q.shape[-2] if q is not None else 0
+    Hkv = k.shape[-2] if k is not None else 0
+    rows = T * (front[0] if len(front) == 2 else 1)
+    fresh = []
+    if q is not None and q_out is None:
+        q_out = torch.empty(front + (H, d), dtype=io, device=dev)
+        fresh.append(q_out)
+    if k is not None and k_out is None:
+        k_out = torch.empty(front + (Hkv, d), dtype=io, device=dev)
+        fresh.append(k_out)
+    strides = (_rows(q, "q", front + (H, d), io, dev) + _rows(k, "k", front + (Hkv, d), io, dev)
+               + _rows(q_out if q is not None else None, "q_out", front + (H, d), io, dev)
+               + _rows(k_out if k is not None else None, "k_out", front + (Hkv, d), io, dev))
+    _i32(positions, "positions", (T,), dev)
+    _check(table.turns, "table.turns", (table.rot_dim // 2,), torch.int64, dev)
+    if rows and H + Hkv:
+        desc = RotaryDesc(rows, T, H, Hkv, d, table.rot_dim, int(table.interleaved), _dtype_code(lead), table.scale, 0,
+                          *strides)
+        with _On(dev, stream) as on:
+            st = getattr(load_library(), name)(ctypes.byref(desc), table.turns.data_ptr(), positions.data_ptr(),
+                                               q.data_ptr() if H else None, k.data_ptr() if Hkv else None,
+                                               q_out.data_ptr() if H else None, k_out.data_ptr() if Hkv else None,
+                                               on.stream)
+            on.keep(*fresh)
+        if st != GDN_OK:
+            raise GdnError(st, f"{name} failed: {status_string(st)}")
+    return q_out if q is not None else None, k_out if k is not None else None
+
+
+def rotary_forward(q, k, positions, table: RotaryTable, *, q_out=None, k_out=None, stream=None):
+    """Rotary positions on q [T, H, d] and k [T, H_kv, d] (gdn_rotary_forward), or on the noisy twins
+    [V, T, H, d], whose views share the positions [T] int32.  Rows and heads may be strided (slices of
+    one projection's output); either of q and k may be None; q_out may be q.  Returns (q_out, k_out)."""
+    return _rotary("gdn_rotary_forward", q, k, positions, table, q_out, k_out, stream)
+
+
+def rotary_backward(dq, dk, positions, table: RotaryTable, *, dq_out=None, dk_out=None, stream=None):
+    """Gradients of rotary_forward's inputs from those of its outputs (gdn_rotary_backward)."""
+    return _rotary("gdn_rotary_backward", dq, dk, positions, table, dq_out, dk_out, stream)
+
+
+# ----------------------------------------------------------------------------- paged key/value cache
+class KvTables:
+    """What kv_extend writes for a step of num_seqs sequences and at most max_new_tokens packed rows:
+    slot_map, positions [max_new_tokens], cu_new [num_seqs + 1], seq_lens [num_seqs], free_left [1]."""
+
+    def __init__(self, num_seqs: int, max_new_tokens: int, device="cuda"):
+        empty = lambda n: torch.empty(n, dtype=torch.int32, device=device)
+        self.slot_map, self.positions, self.cu_new = empty(max_new_tokens), empty(max_new_tokens), empty(num_seqs + 1)
+        self.seq_lens, self.free_left = empty(num_seqs), empty(1)
+
+
+def kv_extend(block_table, seq_lens, new_lens, free_pages, free_count, page_size, tables: KvTables, *, prefix_len=0,
+              device_status=None, stream=None) -> KvTables:
+    """Block tables, slots and positions of a step's new tokens (gdn_kv_extend): block_table [N, W] is
+    extended in place with pages from the top of free_pages [F] (free_count [1] of them are free),
+    tables receives the rest.  The next step takes tables.seq_lens and tables.free_left as its
+    seq_lens and free_count (from another KvTables: outputs must not overlap inputs)."""
+    dev = block_table.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if block_table.ndim != 2:
+        raise ValueError("block_table must be [N, W]")
+    N, W = block_table.shape
+    F, M = free_pages.numel(), tables.slot_map.numel()
+    for t, name, shape in ((block_table, "block_table", (N, W)), (seq_lens, "seq_lens", (N,)), (new_lens, "new_lens", (N,)),
+                           (free_pages, "free_pages", (F,)), (free_count, "free_count", (1,)),
+                           (tables.slot_map, "slot_map", (M,)), (tables.positions, "positions", (M,)),
+                           (tables.cu_new, "cu_new", (N + 1,)), (tables.seq_lens, "tables.seq_lens", (N,)),
+                           (tables.free_left, "free_left", (1,))):
+        _i32(t, name, shape, dev)
+    if device_status is not None:
+        _i32(device_status, "device_status", (1,), dev)
+    desc = KvExtendDesc(N, W, int(page_size), F, M, int(prefix_len), 0, 0)
+    with _On(dev, stream) as on:
+        st = load_library().gdn_kv_extend(ctypes.byref(desc), block_table.data_ptr(), seq_lens.data_ptr(),
+                                          new_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+                                          tables.slot_map.data_ptr(), tables.positions.data_ptr(),
+                                          tables.cu_new.data_ptr(), tables.seq_lens.data_ptr(),
+                                          tables.free_left.data_ptr(),
+                                          None if device_status is None else device_status.data_ptr(), on.stream)
+    if st != GDN_OK:
+        raise GdnError(st, f"gdn_kv_extend failed: {status_string(st)}")
+    return tables
+
+
+def rotary_append(q, k, v, positions, slot_map, table: RotaryTable, k_cache, v_cache, *, q_out=None,
+                  device_status=None, stream=None):
+    """Rotary positions fused with the append to the cache (gdn_rotary_append): q [R, H, d] rotated into
+    q_out, k [R, H_kv, d] rotated into k_cache [P, p, H_kv, d] and v copied into v_cache, at slot_map [R]
+    int32.  Rows with slot -1 are padding and are left as they were.  Returns q_out."""
+    dev, io = q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if q.ndim != 3 or k.ndim != 3 or k_cache.ndim != 4:
+        raise ValueError("q, k and v must be [R, heads, d] and the caches [P, p, H_kv, d]")
+    R, H, d = q.shape
+    Hkv, (P, page) = k.shape[1], k_cache.shape[:2]
+    fresh = q_out is None
+    if fresh:
+        q_out = torch.empty(R, H, d, dtype=io, device=dev)
+    strides = (_rows(q, "q", (R, H, d), io, dev) + _rows(k, "k", (R, Hkv, d), io, dev)
+               + _rows(v, "v", (R, Hkv, d), io, dev) + _rows(q_out, "q_out", (R, H, d), io, dev))
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _check(t, name, (P, page, Hkv, d), io, dev)
+    _i32(positions, "positions", (R,), dev)
+    _i32(slot_map, "slot_map", (R,), dev)
+    if device_status is not None:
+        _i32(device_status, "device_status", (1,), dev)
+    _check(table.turns, "table.turns", (table.rot_dim // 2,), torch.int64, dev)
+    desc = AppendDesc(R, H, Hkv, d, table.rot_dim, int(table.interleaved), page, P, _dtype_code(q), table.scale, *strides)
+    with _On(dev, stream) as on:
+        st = load_library().gdn_rotary_append(ctypes.byref(desc), table.turns.data_ptr(), positions.data_ptr(),
+                                              slot_map.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                              q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                              None if device_status is None else device_status.data_ptr(), on.stream)
+        if fresh:
+            on.keep(q_out)
+    if st != GDN_OK:
+        raise GdnError(st, f"gdn_rotary_append failed: {status_string(st)}")
+    return q_out
+
+
+def make_prefix_attn_desc(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, page_size, num_pages, table_width,
+                          prefix_len, causal, scale=None, dtype_code=GDN_BF16) -> PrefixAttnDesc:
+    return PrefixAttnDesc(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, page_size, num_pages, table_width,
+                          prefix_len, int(bool(causal)), dtype_code, 0.0 if scale is None else float(scale))
+
+
+def prefix_attn_workspace_size(desc: PrefixAttnDesc) -> int:
+    """Workspace bytes of gdn_prefix_attn (0: invalid or unsupported descriptor)."""
+    return int(load_library().gdn_prefix_attn_workspace_size(ctypes.byref(desc)))
+
+
+def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len, block_table, seq_lens, *, causal=True, scale=None,
+                     out=None, workspace: Optional[Workspace] = None, stream=None):
+    """Attention of the L newest tokens of N sequences, q [N, L, H, d] bf16, over a shared prefix (the
+    first prefix_len tokens on the pages prefix_pages) and each sequence's own seq_lens[n] keys through
+    block_table [N, W], in caches [P, p, H_kv, d] (gdn_prefix_attn).  causal=False lets the L tokens see
+    one another (a denoised block).  Returns out [N, L, H, d]."""
+    dev, bf = q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if q.ndim != 4 or k_cache.ndim != 4 or block_table.ndim != 2:
+        raise ValueError("q must be [N, L, H, d], the caches [P, p, H_kv, d] and block_table [N, W]")
+    N, L, H, d = q.shape
+    P, page, Hkv = k_cache.shape[:3]
+    W = block_table.shape[1]
+    _check(q, "q", (N, L, H, d), bf, dev)
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _check(t, name, (P, page, Hkv, d), bf, dev)
+    _i32(block_table, "block_table", (N, W), dev)
+    _i32(seq_lens, "seq_lens", (N,), dev)
+    if scale is not None and not scale > 0:
+        raise ValueError("scale must be positive")
+    prefix_len = int(prefix_len)
+    if prefix_len:
+        _i32(prefix_pages, "prefix_pages", (prefix_pages.numel(),), dev)
+        if prefix_len < 0 or prefix_pages.numel() < -(-prefix_len // page):
+            raise ValueError(f"prefix_pages holds {prefix_pages.numel()} pages of {page} for {prefix_len} tokens")
+    fresh = []
+    if out is None:
+        out = torch.empty(N, L, H, d, dtype=bf, device=dev)
+        fresh.append(out)
+    else:
+        _check(out, "out", (N, L, H, d), bf, dev)
+    desc = make_prefix_attn_desc(N, L, H, Hkv, d, page, P, W, prefix_len, causal, scale, _dtype_code(q))
+    lib = load_library()
+    if workspace is None:
+        nbytes = int(lib.gdn_prefix_attn_workspace_size(ctypes.byref(desc)))
+        ws = torch.empty(max(256, nbytes), dtype=torch.uint8, device=dev)
+        fresh.append(ws)
+    else:
+        ws = workspace.tensor
+        if ws.device != dev:
+            raise ValueError(f"workspace is on {ws.device}, expected {dev}")
+    with _On(dev, stream) as on:
+        st = lib.gdn_prefix_attn(ctypes.byref(desc), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                 prefix_pages.data_ptr() if prefix_len else None, block_table.data_ptr() if W else None,
+                                 seq_lens.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(), on.stream)
+        on.keep(*fresh)
+    if st != GDN_OK:
+        raise GdnError(st, f"gdn_prefix_attn failed: {status_string(st)}")
+    return out
