@@ -10,13 +10,14 @@
 // of ALL sequences are the rows of one matrix, so each prefix key is read once per 256 rows
 // instead of once per sequence, and the product is a real matrix product for tcgen05.
 //
-// gdn_tile_attn_kernel -- one CTA = up to 256 query rows (two 128-row tiles) x a range of 128-key
-// tiles of one key/value head.  Warp 8 loads K and V tiles page by page by TMA into a ring of
-// five slots; warp 9 issues the MMAs; warps 0-3 and 4-7 are the softmax of row tile A and B (thread =
-// row = TMEM lane).  The tensor pipe runs S = Q K^T and O += P V of one tile while the other tile's
-// softmax runs: S_A, S_B, then per key tile PV_A, S_A(next), PV_B, S_B(next).  P (bf16) overwrites
-// the first 64 TMEM columns of its S; MMAs of one issuing thread run in order, so S(next) follows
-// the PV that reads it, and a thread that sees S(next) also knows that PV is done and may rescale O.
+// gdn_tile_attn_kernel -- one CTA = up to 256 query rows (row tiles A and B of 128) x a range of 128-key
+// tiles of one key/value head.  Warp 16 loads K and V tiles page by page by TMA into a ring of five slots;
+// warp 17 issues the products S = Q K^T, warp 19 the products O += P V, warp 18 cleans V rows that must not
+// be seen; warps 0-7 and 8-15 are the softmax of A and B (a row = a TMEM lane is shared by two threads,
+// 64 keys each).  Tensor memory holds one S (fp32), used by A and B in turn, and P (bf16) and O of each.  S
+// goes to registers at once, so the S of the next key tile is there when the softmax of this one ends, and
+// a softmax never waits for its own P V.  Two issuing warps, so that the tensor pipe has products of one while
+// the other waits on a barrier.
 //
 // gdn_warp_attn_kernel -- few query rows of a key list (L (H / H_kv) <= 16: a decode step): bound by
 // reading K and V, and a 128-row tile would be padding.  One CTA = (key list, key/value head, split),
@@ -52,7 +53,11 @@ using namespace sm100;
 constexpr int kTile = 128;                     // keys of a tile, rows of a row tile
 constexpr int kRows = 2 * kTile;               // rows of a CTA
 constexpr int kStages = 5;                     // K and V tiles in flight
-constexpr int kTThreads = 320;
+constexpr int kTThreads = 640;                 // 16 softmax warps, load, MMA, two idle (register shares go by four warps)
+// Registers a thread: the launch gives 96 (65536 / 640, in eights); the softmax warps hold half a row of
+// S and take what the load and MMA warps give up.
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 104, kRegsOther = 56;
+static_assert(4 * kRegsSoftmax + kRegsOther <= 5 * kRegsLaunch, "a warpgroup would wait for registers for ever");
 constexpr int kWKeys = 64;                     // gdn_warp_attn_kernel: keys of a tile (16 per warp)
 constexpr int kWThreads = 160;                 // four warps of arithmetic and one that loads
 constexpr int kWRows = 16;                     // most query rows
@@ -63,17 +68,22 @@ constexpr int kMaxSplits = 64;
 constexpr float kMargin = 8.f;                 // log2 units by which scores may pass the reference max
 constexpr uint32_t kPWaitIters = 1u << 22;
 
+// An item's status word: a gdn_status, a mark, and from bit 16 on the site of a wait that gave up.
+constexpr int kItemNonfinite = 1 << 8;         // among the sequence's newest values were non-finite ones
+
 struct PrefixParams {
     const __nv_bfloat16 *q, *v_cache;
     __nv_bfloat16 *out;
     const int32_t *prefix_pages, *block_table, *seq_lens;
     WorkspaceHeader *ws;
-    int32_t *nonfinite;                        // [N]: the newest values of sequence n hold non-finite ones
+    int32_t *item_status;                      // [items]: what went wrong in a CTA, see kItemNonfinite
     float2 *part_ml;                           // [parts][rows] (m, l)
     float *part_o;                             // [parts][rows][d]
     int64_t rows;                              // N L H
     int32_t N, L, H, Hkv, G, W, page, pages, prefix, causal;
-    int32_t prefix_items, prefix_tiles, prefix_splits, own_tiles, own_splits;   // *_tiles: CTAs over the rows
+    int32_t first_item, items_of_prefix;       // this launch's first item; items [0, items_of_prefix) are the prefix's
+    int32_t prefix_tiles, prefix_splits, own_tiles, own_splits;   // *_tiles: CTAs over the rows
+    int32_t prefix_rows, own_rows;             // rows of such a CTA
     float scale_log2;
 };
 
@@ -88,6 +98,60 @@ __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
     return *reinterpret_cast<uint32_t *>(&p);
 }
 
+// 32 lanes x 16 consecutive 32-bit TMEM columns.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+          "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// One lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// Bounded wait in one piece: true once the phase with this parity is complete.
+__device__ __forceinline__ bool mbar_wait_some(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, 0;\n\t"
+        "again:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra done;\n\t"
+        "add.u32 n, n, 1;\n\t"
+        "setp.lt.u32 q, n, 16;\n\t"
+        "@q bra again;\n\t"
+        "done:\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Two fp32 values in one 64-bit register, and the packed arithmetic on them.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 f2_of(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f2_get(f2 x, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x)); }
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 // Own tokens of sequence n; -1 when the length is out of range.
 __device__ __forceinline__ int own_len(const PrefixParams &P, int n) {
     const int s = P.seq_lens[n];
@@ -101,12 +165,19 @@ struct Item {
     const int32_t *list;                       // page ids
 };
 
+// Dependent launches.  A call's kernels overlap: each lets the next one's CTAs start as soon as its own have
+// all started.  The first kernel of a call waits for the work before it (the inputs, an earlier call's use of the
+// workspace) and only then lets the next one start, so the second kernel may read inputs and write its parts at
+// once; it waits for the first one before it ends, and the combine kernel for the second.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // KEYS of a key tile, ROWS of a CTA; splits of own keys have at least MIN tiles.
 template <int KEYS, int ROWS, int MIN>
 __device__ __forceinline__ Item item_of(const PrefixParams &P, int b) {
     Item w;
     const int per_seq = P.L * P.G;
-    if (b < P.prefix_items) {                  // row tiles fastest: those that run together share keys
+    if (b < P.items_of_prefix) {                  // row tiles fastest: those that run together share keys
         const int tile = b % P.prefix_tiles, rest = b / P.prefix_tiles;
         const int split = rest % P.prefix_splits;
         w.hk = rest / P.prefix_splits;
@@ -120,7 +191,7 @@ __device__ __forceinline__ Item item_of(const PrefixParams &P, int b) {
         w.t1 = (int)((int64_t)nt * (split + 1) / P.prefix_splits);
         w.list = P.prefix_pages;
     } else {
-        b -= P.prefix_items;
+        b -= P.items_of_prefix;
         const int tile = b % P.own_tiles;
         b /= P.own_tiles;
         w.hk = b % P.Hkv;
@@ -145,6 +216,40 @@ __device__ __forceinline__ int64_t row_of(const PrefixParams &P, int hk, int row
     return (int64_t)nl * P.H + hk * P.G + (row - nl * P.G);
 }
 
+// Half a row of S, x (-inf where a key is not visible), to P = 2^(x scale - m_ref) as bf16 pairs in the TMEM
+// columns [tp, tp + 32), which may be written once free() has returned: ls = the sum of P, mt = the largest
+// x in log2 units.  Bound by the exponential unit (8 clocks a warp instruction); taking a share of the
+// exponentials as polynomials on the FMA pipe gained nothing.
+template <typename FREE>
+__device__ __forceinline__ void softmax_half(const float (&x)[2][32], float scale, float m_ref, uint32_t tp, float &ls,
+                                             float &mt, const FREE &free) {
+    const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+    const f2 scale2 = f2_of(scale, scale), shift2 = f2_of(-mu, -mu);
+    f2 sum[4] = {0, 0, 0, 0};
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float x0 = x[c][2 * e], x1 = x[c][2 * e + 1];
+            mx[e & 3] = fmaxf(mx[e & 3], fmaxf(x0, x1));
+            float p0, p1;
+            f2_get(f2_fma(f2_of(x0, x1), scale2, shift2), p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            sum[e & 3] = f2_add(sum[e & 3], f2_of(p0, p1));
+            pk[e] = pack_bf2(p0, p1);
+        }
+        if (c == 0) free();
+        tmem_st16(tp + 16 * c, pk);
+    }
+    float ls1;
+    f2_get(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), ls, ls1);
+    ls += ls1;
+    mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+}
+
 struct PrefixMaps {
     CUtensorMap k, v;                          // [P p, H_kv, d], box: 64 columns x 1 head x min(p, 64) rows
 };
@@ -154,295 +259,378 @@ __global__ void __launch_bounds__(kTThreads, 1)
 gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ PrefixMaps M) {
     constexpr int kHalves = D / 64;
     constexpr int kTileBytes = kTile * D * 2;
-    constexpr uint32_t T_S = 0, T_O = 256;     // TMEM columns: S of A, S of B, O of A, O of B (128 apart)
+    constexpr uint32_t T_S = 0, T_P = 128, T_O = 256;    // TMEM columns: S; P of A and B (64 apart); O of A and B (128 apart)
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
     uint8_t *sm_q = sm, *sm_kv = sm + 2 * kTileBytes;
-    __shared__ uint64_t full[kStages], empty[kStages], bar_q, bar_s[2], bar_p[2], bar_o[2], bar_drain;
+    __shared__ uint64_t full[kStages], empty[kStages];
+    // S of A / B is complete; it is in registers; P of A / B is written; P V is done; V is cleaned
+    __shared__ uint64_t bar_s[2], bar_r[2], bar_p[2], bar_o[2], bar_clean, bar_drain[2];
+    __shared__ float s_pair[kRows];            // between a row's two threads: maxima, at the end a sum
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort;
+    __shared__ int s_abort, s_status;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Item w = item_of<kTile, kRows, 1>(P, blockIdx.x);
+    const int item = P.first_item + blockIdx.x;
+    if (P.first_item == 0) grid_wait();
+    grid_next();
+    if (item == 0 && tid == 0) P.ws->status = P.ws->timeout_where = 0;
+    const Item w = item_of<kTile, kRows, 1>(P, item);
     const int tiles = w.t1 - w.t0;
     float2 *ml = P.part_ml + w.part * P.rows;
     if (tiles == 0) {                          // an empty part: nothing visible
         for (int r = tid; r < w.nrows; r += kTThreads) ml[row_of(P, w.hk, w.row0 + r)] = make_float2(-INFINITY, 0.f);
+        if (tid == 0) P.item_status[item] = 0;
+        grid_wait();
         return;
     }
     const int two = w.nrows > kTile;           // row tile B is in use
 
-    if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+    // The ring's order is the order of use: K0 K1 V0 K2 V1 ... V(last).  Loads tile i of the ring (warp 16):
+    // lane = (half, box), a box is min(p, 64) rows of one page, 64 columns; rows past the end read as zeros.
+    auto v_at = [&](int j) { return j + 1 < tiles ? 2 * j + 2 : 2 * j + 1; };
+    auto load = [&](int i) {
+        const int box_rows = min(P.page, 64), boxes = kTile / box_rows;
+        const int box = lane % boxes, half = lane / boxes;
+        const bool value = i > 0 && ((i & 1) == 0 || i == 2 * tiles - 1);
+        const int j = w.t0 + (value ? (i == 2 * tiles - 1 ? tiles - 1 : i / 2 - 1) : (i + 1) / 2);
+        const int slot = i % kStages, key = j * kTile + box * box_rows;
+        int row = P.pages * P.page;
+        if (half < kHalves && key < w.keys) {
+            const int id = w.list[key / P.page];
+            if (id >= 0 && id < P.pages) row = id * P.page + key % P.page;
+            else atomicOr(&s_status, (int)GDN_ERR_INVALID_ARG);
         }
-        mbar_init(&bar_q, 8);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar_s[i], 1);
-            mbar_init(&bar_p[i], 4);
-            mbar_init(&bar_o[i], 1);
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], kTileBytes);
+        __syncwarp();
+        if (half < kHalves)
+            tma_load_3d(sm_kv + slot * kTileBytes + half * (kTile * 128) + box * box_rows * 128, value ? &M.v : &M.k,
+                        &full[slot], half * 64, w.hk, row);
+        __syncwarp();
+    };
+    if (warp == 16) {
+        if (lane == 0) {
+            for (int i = 0; i < kStages; ++i) {
+                mbar_init(&full[i], 1);
+                mbar_init(&empty[i], 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&bar_s[i], 1);
+                mbar_init(&bar_r[i], 8);
+                mbar_init(&bar_p[i], 8);
+                mbar_init(&bar_o[i], 1);
+                mbar_init(&bar_drain[i], 1);
+            }
+            mbar_init(&bar_clean, 1);
+            fence_mbar_init();
+            fence_async_smem();
+            s_abort = s_status = 0;
         }
-        mbar_init(&bar_drain, 1);
-        fence_mbar_init();
-        s_abort = 0;
-    }
-    __syncwarp();
-    if (warp == 0) {
+        __syncwarp();
+        for (int i = 0; i < min(kStages, 2 * tiles); ++i) load(i);         // beside the queries' loads
+    } else if (warp == 17) {
         tmem_alloc(&s_tmem, 512);
         tmem_relinquish();
+    } else if (warp < 16) {
+        // queries: D / 8 chunks of 16 bytes a row, a pass covers 512 / (D / 8) rows; all loads ahead of the stores
+        constexpr int kChunks = D / 8, kPass = 512 / kChunks, kBatch = kTile / kPass;
+        const int c = tid % kChunks, r0 = tid / kChunks;
+        int nl = (w.row0 + r0) / P.G, g = (w.row0 + r0) - nl * P.G;       // (n, l) and head of the row
+        const int dn = kPass / P.G, dg = kPass - dn * P.G;               // the same of kPass rows
+        const __nv_bfloat16 *head = P.q + (int64_t)w.hk * P.G * D + c * 8;
+#pragma unroll 1
+        for (int t = 0; t <= two; ++t) {
+            uint4 u[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                u[i] = make_uint4(0, 0, 0, 0);
+                if (t * kTile + r0 + i * kPass < w.nrows)
+                    u[i] = *reinterpret_cast<const uint4 *>(head + ((int64_t)nl * P.H + g) * D);
+                nl += dn;
+                if ((g += dg) >= P.G) g -= P.G, ++nl;
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                *reinterpret_cast<uint4 *>(sm_q + t * kTileBytes + (c >> 3) * (kTile * 128) + sw128_off(r0 + i * kPass, c & 7)) = u[i];
+        }
+        fence_async_smem();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = s_tmem;
 
-    // Bounded wait of a whole warp: false (in every lane) when it gave up, or another warp did.
-    auto wait_ok = [&](uint64_t *bar, uint32_t parity, int where) {
-        bool ok = false;
-        for (uint32_t it = 0; it < kPWaitIters; ++it) {
-            if ((ok = mbar_try_wait(bar, parity))) break;
-            if ((it & 15) == 15 && *reinterpret_cast<volatile int *>(&s_abort)) break;
+    // Bounded wait.  A wait that gives up marks the CTA as stopping and returns; every further wait gives up at
+    // once.  Loads and products stop at the end of the key tile; the softmax warps, which meet at the barriers of
+    // their pairs, run through their tiles (on unspecified data) and write nothing.
+    auto stopped = [&] { return *reinterpret_cast<volatile int *>(&s_abort) != 0; };
+    auto wait = [&](uint64_t *bar, uint32_t parity, int where) {
+        if (mbar_try_wait(bar, parity)) return;
+        for (uint32_t it = 0; it < kPWaitIters / 16; ++it) {
+            if (mbar_wait_some(bar, parity)) return;
+            if (stopped()) return;
         }
-        if (!ok && atomicExch(&s_abort, 1) == 0) {
-            atomicExch(&P.ws->status, (int)GDN_ERR_TIMEOUT);
-            atomicExch(&P.ws->timeout_where, where);
-        }
-        return __all_sync(0xffffffffu, ok) != 0;
+        if (atomicExch(&s_abort, 1) == 0) atomicExch(&s_status, (int)GDN_ERR_TIMEOUT | where << 16);
     };
+    // V rows from key `newest` on are not for every query row (see the file comment): warp 10 cleans their tiles
+    const int newest = (w.n >= 0 && P.causal) ? w.keys - (P.L - 1) : w.keys;
 
-    if (warp == 8) {
+    if (warp == 16) {
         // ---------------------------------------------------------------- loads
-        // lane = (half, box): a box is min(p, 64) rows of one page, 64 columns
-        const int box_rows = min(P.page, 64), boxes = kTile / box_rows;
-        const int box = lane % boxes, half = lane / boxes;
-        const bool mine = half < kHalves;
-        const int oob = P.pages * P.page;      // a row past the end: reads as zeros
-        int issued = 0;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        int issued = min(kStages, 2 * tiles);
         for (; issued < 2 * tiles; ++issued) {
-            const int j = w.t0 + (issued >> 1), slot = issued % kStages;
-            const int key = j * kTile + box * box_rows;
-            int row = oob;
-            if (mine && key < w.keys) {
-                const int id = w.list[key / P.page];
-                if (id >= 0 && id < P.pages) row = id * P.page + key % P.page;
-                else atomicCAS(&P.ws->status, 0, (int)GDN_ERR_INVALID_ARG);
-            }
-            if (issued >= kStages && !wait_ok(&empty[slot], (issued / kStages - 1) & 1, 1)) break;
-            if (lane == 0) mbar_arrive_expect_tx(&full[slot], kTileBytes);
+            wait(&empty[issued % kStages], (issued / kStages - 1) & 1, 1);
             __syncwarp();
-            if (mine)
-                tma_load_3d(sm_kv + slot * kTileBytes + half * (kTile * 128) + box * box_rows * 128,
-                            (issued & 1) ? &M.v : &M.k, &full[slot], half * 64, w.hk, row);
-            __syncwarp();
+            if (__any_sync(0xffffffffu, stopped())) break;     // the slot may still be in use
+            load(issued);
         }
-        if (issued < 2 * tiles && lane == 0)   // gave up: the loads in flight still land
+        if (__any_sync(0xffffffffu, stopped()) && lane == 0)   // gave up: the loads in flight still land
             for (int i = max(0, issued - kStages); i < issued; ++i)
                 mbar_wait(&full[i % kStages], (i / kStages) & 1, kDrainWaitIters);
-    } else if (warp == 9) {
-        // ---------------------------------------------------------------- MMAs
-        constexpr uint32_t idesc_s = make_idesc_bf16(128, 128, 0, 0);
-        constexpr uint32_t idesc_o = make_idesc_bf16(128, D, 0, 1);
-        const uint64_t dq = make_sdesc(smem_u32(sm_q), 16, 1024);
-        auto score = [&](int t, int slot) {    // S_t = Q_t K^T
-            const uint64_t dk = make_sdesc(smem_u32(sm_kv + slot * kTileBytes), 16, 1024);
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-                mma_bf16(tb + T_S + 128 * t, dq + ((t * kTileBytes + off) >> 4), dk + (off >> 4), idesc_s, kk > 0);
-            }
+    } else if (warp == 17 || warp == 19) {
+        // ---------------------------------------------------------------- products: S (warp 17), P V (warp 19)
+        // Two streams, so that one's products run while the other waits on a barrier; warp-uniform, with few
+        // instructions between the products (a single thread's chain of address arithmetic and branches
+        // cost more than the products that it fed).
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        constexpr uint32_t kStep = kTileBytes >> 4;
+        int slot = 0, left = tiles;
+        uint32_t phase = 0;
+        auto advance = [&](int n) {            // n tiles on in the ring
+            slot += n;
+            if (slot >= kStages) slot -= kStages, phase ^= 1;
         };
-        auto value = [&](int t, int slot, bool more) {   // O_t (+)= P_t V
-            const uint64_t dv = make_sdesc(smem_u32(sm_kv + slot * kTileBytes), kTile * 128, 1024);
-            for (int kk = 0; kk < 8; ++kk)
-                mma_bf16_ts(tb + T_O + 128 * t, tb + T_S + 128 * t + kk * 8, dv + ((kk * 2048) >> 4), idesc_o, more || kk > 0);
-        };
-        bool ok = wait_ok(&bar_q, 0, 2) && wait_ok(&full[0], 0, 3);
-        if (ok) {
-            tc_fence_after();
-            if (lane == 0) {
-                score(0, 0);
-                mma_commit(&bar_s[0]);
-                if (two) {
-                    score(1, 0);
-                    mma_commit(&bar_s[1]);
+        if (warp == 17) {
+            constexpr uint32_t idesc = make_idesc_bf16(128, 128, 0, 0);
+            const uint64_t dq = make_sdesc(smem_u32(sm_q), 16, 1024), dk = make_sdesc(smem_u32(sm_kv), 16, 1024);
+            uint32_t odd = 0;                  // parity of the key tile
+            for (int j = 0; j < tiles; ++j, odd ^= 1) {
+                wait(&full[slot], phase, 2);
+                for (int t = 0; t <= two; ++t) {
+                    // the S before this one (of the other row tile, or of this one) is in registers
+                    if (t == 1) wait(&bar_r[0], odd, 3);
+                    else if (j > 0) wait(&bar_r[two], odd ^ 1, 3);
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
+                            mma_bf16(tb + T_S, dq + t * kStep + off, dk + slot * kStep + off, idesc, kk > 0);
+                        }
+                        mma_commit(&bar_s[t]);
+                        if (t == two) mma_commit(&empty[slot]);
+                    }
+                    __syncwarp();
                 }
-                mma_commit(&empty[0]);
+                advance(j == 0 ? 1 : 2);
+                if (__any_sync(0xffffffffu, stopped())) break;
             }
-            __syncwarp();
+        } else {
+            constexpr uint32_t idesc = make_idesc_bf16(128, D, 0, 1);
+            const uint64_t dv = make_sdesc(smem_u32(sm_kv), kTile * 128, 1024);
+            int end = (w.t0 + 1) * kTile, cleaned = 0;
+            slot = tiles > 1 ? 2 : 1;
+            for (int j = 0; j < tiles; ++j, end += kTile) {
+                wait(&full[slot], phase, 4);
+                if (end > newest) wait(&bar_clean, cleaned++ & 1, 5);
+                for (int t = 0; t <= two; ++t) {
+                    wait(&bar_p[t], j & 1, 6);
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_bf16_ts(tb + T_O + 128 * t, tb + T_P + 64 * t + kk * 8, dv + slot * kStep + kk * 128, idesc, j > 0 || kk > 0);
+                        mma_commit(&bar_o[t]);
+                        if (t == two) mma_commit(&empty[slot]);
+                    }
+                    __syncwarp();
+                }
+                advance(--left > 1 ? 2 : 1);   // the last V follows the one before it
+                if (__any_sync(0xffffffffu, stopped())) break;
+            }
         }
-        for (int j = 0; ok && j < tiles; ++j) {
-            const int iv = 2 * j + 1, ik = 2 * j + 2, sv = iv % kStages, sk = ik % kStages;
-            const bool next = j + 1 < tiles;
-            if (!(ok = wait_ok(&full[sv], (iv / kStages) & 1, 4))) break;
-            // V rows that a row of the tile must not see
-            const int key0 = (w.t0 + j) * kTile;
+        if (__any_sync(0xffffffffu, stopped()) && elect_one()) {       // gave up: the MMAs in flight still end
+            mma_commit(&bar_drain[warp == 19]);
+            mbar_wait(&bar_drain[warp == 19], 0, kDrainWaitIters);
+        }
+        __syncwarp();
+    } else if (warp == 18) {
+        // ---------------------------------------------------------------- V rows not to be seen
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        for (int j = 0; j < tiles; ++j) {
+            if ((w.t0 + j + 1) * kTile <= newest) continue;
+            const int iv = v_at(j), sv = iv % kStages, key0 = (w.t0 + j) * kTile;
+            wait(&full[sv], (iv / kStages) & 1, 9);
+            __syncwarp();
+            if (__any_sync(0xffffffffu, stopped())) break;
             uint8_t *v = sm_kv + sv * kTileBytes;
             const int last = min(kTile, w.keys - key0);          // rows [last, 128) are behind the list's end
-            const int newest = (w.n >= 0 && P.causal) ? w.keys - (P.L - 1) : w.keys;
-            if (last < kTile || newest < key0 + last) {
-                for (int i = lane; i < (kTile - last) * (D / 8); i += 32) {
-                    const int r = last + i / (D / 8), c = i % (D / 8);
-                    *reinterpret_cast<uint4 *>(v + (c >> 3) * (kTile * 128) + sw128_off(r, c & 7)) = make_uint4(0, 0, 0, 0);
-                }
-                const int lo = max(newest - key0, 0);
-                bool found = false;
-                for (int i = lane; i < (last - lo) * (D / 8); i += 32) {
-                    const int r = lo + i / (D / 8), c = i % (D / 8);
-                    uint32_t *p = reinterpret_cast<uint32_t *>(v + (c >> 3) * (kTile * 128) + sw128_off(r, c & 7));
+            for (int i = lane; i < (kTile - last) * (D / 8); i += 32) {
+                const int r = last + i / (D / 8), c = i % (D / 8);
+                *reinterpret_cast<uint4 *>(v + (c >> 3) * (kTile * 128) + sw128_off(r, c & 7)) = make_uint4(0, 0, 0, 0);
+            }
+            const int lo = max(newest - key0, 0);                // rows [lo, last) are visible to some rows only
+            bool found = false;
+            for (int i = lane; i < (last - lo) * (D / 8); i += 32) {
+                const int r = lo + i / (D / 8), c = i % (D / 8);
+                uint32_t *p = reinterpret_cast<uint32_t *>(v + (c >> 3) * (kTile * 128) + sw128_off(r, c & 7));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t x = p[e];
-                        const bool a = (x & 0x7f80u) == 0x7f80u, b = (x & 0x7f800000u) == 0x7f800000u;
-                        if (a) x &= 0xffff0000u;
-                        if (b) x &= 0xffffu;
-                        if (a || b) {
-                            p[e] = x;
-                            found = true;
-                        }
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t x = p[e];
+                    const bool a = (x & 0x7f80u) == 0x7f80u, b = (x & 0x7f800000u) == 0x7f800000u;
+                    if (a) x &= 0xffff0000u;
+                    if (b) x &= 0xffffu;
+                    if (a || b) {
+                        p[e] = x;
+                        found = true;
                     }
                 }
-                if (found) P.nonfinite[w.n] = 1;
-                fence_async_smem();
-                __syncwarp();
             }
-            if (next && !(ok = wait_ok(&full[sk], (ik / kStages) & 1, 5))) break;
-            for (int t = 0; t <= two; ++t) {
-                if (!(ok = wait_ok(&bar_p[t], j & 1, 6))) break;
-                tc_fence_after();
-                if (lane == 0) {
-                    value(t, sv, j > 0);
-                    if (t == two) mma_commit(&empty[sv]);
-                    if (next) {
-                        score(t, sk);
-                        mma_commit(&bar_s[t]);
-                        if (t == two) mma_commit(&empty[sk]);
-                    } else {
-                        mma_commit(&bar_o[t]);
-                    }
-                }
-                __syncwarp();
-            }
-        }
-        if (!ok && lane == 0) {                // gave up: the MMAs in flight still end
-            mma_commit(&bar_drain);
-            mbar_wait(&bar_drain, 0, kDrainWaitIters);
+            if (found) atomicOr(&s_status, kItemNonfinite);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_clean);
         }
     } else {
-        // ---------------------------------------------------------------- queries, then softmax
-        for (int i = tid; i < (two ? kRows : kTile) * (D / 8); i += 256) {
-            const int r = i / (D / 8), c = i % (D / 8);
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (r < w.nrows) u = *reinterpret_cast<const uint4 *>(P.q + row_of(P, w.hk, w.row0 + r) * D + c * 8);
-            *reinterpret_cast<uint4 *>(sm_q + (r >> 7) * kTileBytes + (c >> 3) * (kTile * 128) + sw128_off(r & 127, c & 7)) = u;
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_q);
-
-        const int t = warp >> 2, quad = warp & 3, r = tid;       // row of the CTA = thread
+        // ---------------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        const int t = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3;
+        const int r = t * kTile + quad * 32 + lane;                            // row of the CTA
+        const int pair = 1 + t * 4 + quad;                                     // named barrier of the rows' two warps
         const bool live = r < w.nrows;
-        const bool warp_live = (warp << 5) < w.nrows;
+        const bool warp_live = t * kTile + quad * 32 < w.nrows;
         // keys [0, sees) are this row's
         int sees = live ? w.keys : 0;
         if (live && w.n >= 0 && P.causal) {
             const int l = ((w.row0 + r) / P.G) % P.L;
             sees = max(0, w.keys - (P.L - 1 - l));
         }
-        const uint32_t ts = tmem_addr(tb, quad * 32, T_S + 128 * t), to = tmem_addr(tb, quad * 32, T_O + 128 * t);
+        const uint32_t ts = tmem_addr(tb, quad * 32, T_S + 64 * half);                     // this thread's half of S,
+        const uint32_t tp = tmem_addr(tb, quad * 32, T_P + 64 * t + 32 * half);            // of P
+        const uint32_t to = tmem_addr(tb, quad * 32, T_O + 128 * t + (D / 2) * half);      // and of O
         const float sl2 = P.scale_log2;
         float m_ref = -INFINITY, l_sum = 0.f;
-        bool ok = true;
         if (t == 0 || two) {
             for (int j = 0; j < tiles; ++j) {
-                if (!(ok = wait_ok(&bar_s[t], j & 1, 7))) break;
+                wait(&bar_s[t], j & 1, 7);
                 __syncwarp();
                 tc_fence_after();
+                float x[2][32];
                 if (warp_live) {
-                    float x[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, x[c]);
+                    tmem_ld32(ts, x[0]);
+                    tmem_ld32(ts + 32, x[1]);
                     tmem_wait_ld();
-                    const int hi = sees - (w.t0 + j) * kTile;    // columns [0, hi) are visible
-                    float mt = -INFINITY;
-                    if (hi >= kTile) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) mt = fmaxf(mt, x[c][e]);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                x[c][e] = 32 * c + e < hi ? x[c][e] : -INFINITY;
-                                mt = fmaxf(mt, x[c][e]);
-                            }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar_r[t]);           // S may be overwritten
+                // P V of the tile before is done: P may be overwritten, O rescaled
+                bool waited = j == 0;
+                auto free = [&] {
+                    if (!waited) {
+                        wait(&bar_o[t], (j - 1) & 1, 8);
+                        __syncwarp();
+                        tc_fence_after();
+                        waited = true;
                     }
-                    mt *= sl2;
-                    float alpha = 1.f;
-                    if (mt > m_ref + kMargin) {
-                        alpha = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - mt);
-                        m_ref = mt;
+                };
+                if (warp_live) {
+                    const int hi = sees - (w.t0 + j) * kTile - 64 * half;      // this half's columns [0, hi) are visible
+                    if (hi < 64) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[c][e] = 32 * c + e < hi ? x[c][e] : -INFINITY;
                     }
-                    const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-                    if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    // P = 2^(s - m) with the reference max of the tiles before, while the tile's own max is
+                    // taken beside it (it would wait for itself in a pass of its own).  Only if that max
+                    // passes the reference by more than the margin is m moved, O and l rescaled and P taken
+                    // again: in a list's first tile, and rarely later.  The rows' two warps decide together.
+                    float ls;
+                    while (true) {
+                        float mt;
+                        softmax_half(x, sl2, m_ref, tp, ls, mt, free);
+                        if (!bar_sync_or(pair, 64, mt > m_ref + kMargin)) break;
+                        if (half == 0) s_pair[r] = mt;
+                        asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+                        if (half == 1) s_pair[r] = mt = fmaxf(mt, s_pair[r]);
+                        asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+                        mt = s_pair[r];
+                        const bool up = mt > m_ref + kMargin;
+                        const float alpha = !up ? 1.f : m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - mt);
+                        if (up) m_ref = mt;
+                        l_sum *= alpha;
+                        tmem_wait_st();
+                        if (j > 0) {
 #pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            float o[32];
-                            tmem_ld32(to + c0, o);
-                            tmem_wait_ld();
+                            for (int c0 = 0; c0 < D / 2; c0 += 32) {
+                                float o[32];
+                                tmem_ld32(to + c0, o);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                            tmem_st32(to + c0, o);
+                                for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                                tmem_st32(to + c0, o);
+                            }
                         }
-                    }
-                    l_sum *= alpha;
-                    float ls = 0.f;
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        float pk[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float p0 = ex2_approx(fmaf(x[2 * hf + e / 16][(2 * e) % 32], sl2, -mu));
-                            const float p1 = ex2_approx(fmaf(x[2 * hf + e / 16][(2 * e) % 32 + 1], sl2, -mu));
-                            ls += p0 + p1;
-                            pk[e] = __uint_as_float(pack_bf2(p0, p1));
-                        }
-                        tmem_st32(ts + 32 * hf, pk);
                     }
                     l_sum += ls;
                     tmem_wait_st();
+                } else {
+                    free();
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar_p[t]);
             }
-            if (ok && (ok = wait_ok(&bar_o[t], 0, 8))) {
-                __syncwarp();
+            wait(&bar_o[t], (tiles - 1) & 1, 10);
+            __syncwarp();
+            if (warp_live && !bar_sync_or(pair, 64, stopped())) {
                 tc_fence_after();
+                if (half == 1) s_pair[r] = l_sum;
+                asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
                 const int64_t row = live ? row_of(P, w.hk, w.row0 + r) : 0;
-                if (m_ref == -INFINITY && l_sum != 0.f) m_ref = 0.f;   // every visible score is NaN: so is the row
-                if (live) ml[row] = make_float2(m_ref, l_sum);
-                float *po = P.part_o + (w.part * P.rows + row) * D;
-                if (warp_live) {
+                if (live && half == 0) {
+                    l_sum += s_pair[r];
+                    if (m_ref == -INFINITY && l_sum != 0.f) m_ref = 0.f;       // every visible score is NaN: so is the row
+                    ml[row] = make_float2(m_ref, l_sum);
+                }
+                // O leaves row by row through shared memory (a lane holds a row: 32 rows at once would be 32
+                // partial lines per store), in the space of this row tile's queries, whose products are done.  It
+                // holds 64 columns of the tile: one half after the other at d = 128.
+                constexpr int kC = D / 8;                        // 16-byte chunks of half a row, chunk c at c ^ (row & 7)
+                float4 *st = reinterpret_cast<float4 *>(sm_q + t * kTileBytes) + quad * 32 * kC;
+                const int rows = min(32, w.nrows - (t * kTile + quad * 32));
+                for (int h = 0; h < 2; ++h) {
+                    if (half == h) {
 #pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 32) {
-                        float o[32];
-                        tmem_ld32(to + c0, o);
-                        tmem_wait_ld();
-                        if (live) {
+                        for (int c0 = 0; c0 < D / 2; c0 += 32) {
+                            float o[32];
+                            tmem_ld32(to + c0, o);
+                            tmem_wait_ld();
 #pragma unroll
                             for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<float4 *>(po + c0 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                                st[lane * kC + (((c0 + e) / 4) ^ (lane & 7))] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                         }
                     }
+                    asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+#pragma unroll 4
+                    for (int i0 = half * 32; i0 < rows * kC; i0 += 64) {
+                        const int i = i0 + lane, rr = min(i / kC, 31), c = i % kC;
+                        const int64_t dst = __shfl_sync(0xffffffffu, row, rr);
+                        if (i < rows * kC)
+                            reinterpret_cast<float4 *>(P.part_o + (w.part * P.rows + dst) * D + (D / 2) * h)[c] = st[rr * kC + (c ^ (rr & 7))];
+                    }
+                    asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
                 }
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tb, 512);
+    if (warp == 17) tmem_dealloc(tb, 512);
+    if (tid == 0) P.item_status[item] = s_status;
+    grid_wait();
 }
 
 // ------------------------------------------------------------------------------------ few rows
@@ -480,14 +668,20 @@ gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t full[kWStages], empty[kWStages];
     __shared__ float2 s_ml[4][kWRows];
-    __shared__ int s_abort;
+    __shared__ int s_abort, s_status;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Item w = item_of<kWKeys, kWRows, kWMinTiles>(P, blockIdx.x);
+    const int item = P.first_item + blockIdx.x;
+    if (P.first_item == 0) grid_wait();
+    grid_next();
+    if (item == 0 && tid == 0) P.ws->status = P.ws->timeout_where = 0;
+    const Item w = item_of<kWKeys, kWRows, kWMinTiles>(P, item);
     const int tiles = w.t1 - w.t0;
     float2 *ml = P.part_ml + w.part * P.rows;
     if (tiles == 0) {                          // an empty part: nothing visible
         if (tid < w.nrows) ml[row_of(P, w.hk, w.row0 + tid)] = make_float2(-INFINITY, 0.f);
+        if (tid == 0) P.item_status[item] = 0;
+        grid_wait();
         return;
     }
     if (tid == 0) {
@@ -496,7 +690,7 @@ gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
             mbar_init(&empty[i], 4);
         }
         fence_mbar_init();
-        s_abort = 0;
+        s_abort = s_status = 0;
     }
     __syncthreads();
 
@@ -506,10 +700,7 @@ gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
             if ((ok = mbar_try_wait(bar, parity))) break;
             if ((it & 15) == 15 && *reinterpret_cast<volatile int *>(&s_abort)) break;
         }
-        if (!ok && atomicExch(&s_abort, 1) == 0) {
-            atomicExch(&P.ws->status, (int)GDN_ERR_TIMEOUT);
-            atomicExch(&P.ws->timeout_where, where);
-        }
+        if (!ok && atomicExch(&s_abort, 1) == 0) atomicExch(&s_status, (int)GDN_ERR_TIMEOUT | where << 16);
         return __all_sync(0xffffffffu, ok) != 0;
     };
 
@@ -538,7 +729,7 @@ gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
             if (mine && key < w.keys) {
                 const int id = w.list[key / P.page];
                 if (id >= 0 && id < P.pages) row = id * P.page + key % P.page;
-                else atomicCAS(&P.ws->status, 0, (int)GDN_ERR_INVALID_ARG);
+                else atomicOr(&s_status, (int)GDN_ERR_INVALID_ARG);
             }
             if (issued >= kWStages && !wait_ok(&empty[slot], (issued / kWStages - 1) & 1, 11)) break;
             if (lane == 0) mbar_arrive_expect_tx(&full[slot], 2 * kTileBytes);
@@ -616,7 +807,7 @@ gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
                             }
                         }
                     }
-                    if (found) P.nonfinite[w.n] = 1;
+                    if (found) atomicOr(&s_status, kItemNonfinite);
                     fence_async_smem();        // before the slot's next load
                     __syncwarp();
                 }
@@ -717,50 +908,99 @@ gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
         }
         reinterpret_cast<float4 *>(P.part_o + (w.part * P.rows + row_of(P, w.hk, w.row0 + row)) * D)[c] = o;
     }
+    if (tid == 0) P.item_status[item] = s_status;
+    grid_wait();
 }
 
-// One warp per row (n, l, h): lane holds D / 32 columns.
+// The item that made part `p` of row (n, l, h).
+__device__ __forceinline__ int64_t item_at(const PrefixParams &P, int p, int n, int l, int h) {
+    const int hk = h / P.G, in_seq = l * P.G + (h - hk * P.G);
+    if (p < P.prefix_splits)
+        return ((int64_t)hk * P.prefix_splits + p) * P.prefix_tiles + ((int64_t)n * P.L * P.G + in_seq) / P.prefix_rows;
+    return P.items_of_prefix +
+           (((int64_t)n * P.own_splits + (p - P.prefix_splits)) * P.Hkv + hk) * P.own_tiles + in_seq / P.own_rows;
+}
+
+// One warp per row (n, l, h): lane holds D / 32 columns.  A lane first takes the (m, l) of parts of its own, so
+// that the parts' rows are read without waiting for one another.
 template <int D>
-__global__ void __launch_bounds__(256) gdn_attn_combine_kernel(const __grid_constant__ PrefixParams P, int parts) {
+__global__ void __launch_bounds__(128) gdn_attn_combine_kernel(const __grid_constant__ PrefixParams P, int parts) {
     constexpr int C = D / 32;
-    const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
+    const int64_t row = ((int64_t)blockIdx.x * 128 + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
-    if (row >= P.rows) return;
     const int h = (int)(row % P.H), l = (int)(row / P.H % P.L), n = (int)(row / P.H / P.L);
+    grid_wait();
+    if (row >= P.rows) return;
     const int s = own_len(P, n);
-    if (s < 0) {
-        if (lane == 0) atomicCAS(&P.ws->status, 0, (int)GDN_ERR_INVALID_ARG);
-        return;
-    }
-    float m = -INFINITY;
-    for (int p = lane; p < parts; p += 32) m = fmaxf(m, P.part_ml[p * P.rows + row].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float acc[C], sum = 0.f;
+    float m = -INFINITY, sum = 0.f, acc[C];
+    int status = s < 0 ? (int)GDN_ERR_INVALID_ARG : 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] = 0.f;
-    if (m != -INFINITY) {
-        for (int p = 0; p < parts; ++p) {
-            const float2 a = P.part_ml[p * P.rows + row];
-            if (a.x == -INFINITY) continue;
-            const float f = ex2_approx(a.x - m);
-            sum = fmaf(f, a.y, sum);
-            const float *o = P.part_o + (p * P.rows + row) * D + lane * C;
-            float x[C];
-            if constexpr (C == 4) {
-                const float4 u = *reinterpret_cast<const float4 *>(o);
-                x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
-            } else {
-                const float2 u = *reinterpret_cast<const float2 *>(o);
-                x[0] = u.x, x[1] = u.y;
+    for (int p0 = 0; p0 < parts; p0 += 32) {       // 32 parts at a time, joined to what came before
+        float2 a = make_float2(-INFINITY, 0.f);
+        if (p0 + lane < parts) {
+            a = P.part_ml[(p0 + lane) * P.rows + row];
+            status |= P.item_status[item_at(P, p0 + lane, n, l, h)];
+        }
+        float top = a.x;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = fmaxf(top, m);
+        if (top == -INFINITY) continue;
+        const float back = m == -INFINITY ? 0.f : ex2_approx(m - top);
+        m = top;
+        const float f = a.x == -INFINITY ? 0.f : ex2_approx(a.x - top);
+        float part = a.x == -INFINITY ? 0.f : f * a.y;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+        sum = sum * back + part;
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] *= back;
+        uint32_t some = __ballot_sync(0xffffffffu, a.x != -INFINITY);     // parts that see a key
+        while (some) {
+            float x[4][C], g[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {          // four rows on their way at a time
+                const int p = some ? __ffs(some) - 1 : -1;
+                some &= some - 1;
+                g[i] = __shfl_sync(0xffffffffu, f, max(p, 0));
+                if (p < 0) g[i] = 0.f;
+#pragma unroll
+                for (int c = 0; c < C; ++c) x[i][c] = 0.f;
+                if (p >= 0) {
+                    const float *o = P.part_o + ((p0 + p) * P.rows + row) * D + lane * C;
+                    if constexpr (C == 4) {
+                        const float4 u = *reinterpret_cast<const float4 *>(o);
+                        x[i][0] = u.x, x[i][1] = u.y, x[i][2] = u.z, x[i][3] = u.w;
+                    } else {
+                        const float2 u = *reinterpret_cast<const float2 *>(o);
+                        x[i][0] = u.x, x[i][1] = u.y;
+                    }
+                }
             }
 #pragma unroll
-            for (int c = 0; c < C; ++c) acc[c] = fmaf(f, x[c], acc[c]);
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < C; ++c) acc[c] = fmaf(g[i], x[i][c], acc[c]);
         }
+    }
+    status = __reduce_or_sync(0xffffffffu, status);
+    if (status) {
+        if (lane == 0 && (status & 0xff)) {
+            if ((status & 0xff) == GDN_ERR_INVALID_ARG) {
+                atomicCAS(&P.ws->status, 0, (int)GDN_ERR_INVALID_ARG);
+            } else {                               // a wait gave up somewhere (perhaps beside bad pages)
+                atomicExch(&P.ws->status, (int)GDN_ERR_TIMEOUT);
+                atomicExch(&P.ws->timeout_where, status >> 16);
+            }
+        }
+        if (s < 0) return;
+    }
+    if (m != -INFINITY) {
         const float inv = 1.f / sum;
 #pragma unroll
         for (int c = 0; c < C; ++c) acc[c] *= inv;
-        if (P.causal && P.L > 1 && P.nonfinite[n]) {   // set to zero in the product: they reach the rows that see them
+        if (status & kItemNonfinite) {             // set to zero in the product: they reach the rows that see them
             const int sees = max(0, s - (P.L - 1 - l));
             for (int key = max(0, s - (P.L - 1)); key < sees; ++key) {
                 const int id = P.block_table[(int64_t)n * P.W + key / P.page];
@@ -828,7 +1068,7 @@ struct Plan {
     bool prefix_warp, own_warp;                // by gdn_warp_attn_kernel (else gdn_tile_attn_kernel)
     int prefix_tiles, prefix_splits, own_tiles, own_splits, parts;
     int64_t prefix_items, own_items;
-    size_t off_nonfinite, off_ml, off_o, bytes;
+    size_t off_status, off_ml, off_o, bytes;
 };
 
 // Splits of `tiles` key tiles over `base` equal work items: waves of CTAs times a CTA's tiles, three more
@@ -870,8 +1110,8 @@ Plan plan_of(const gdn_prefix_attn_desc *D) {
     p.prefix_items = (int64_t)D->num_kv_heads * p.prefix_tiles * p.prefix_splits;
     p.own_items = (int64_t)D->num_seqs * D->num_kv_heads * p.own_tiles * p.own_splits;
     p.parts = p.prefix_splits + p.own_splits;
-    p.off_nonfinite = sizeof(WorkspaceHeader);
-    p.off_ml = p.off_nonfinite + round256((size_t)D->num_seqs * 4);
+    p.off_status = sizeof(WorkspaceHeader);
+    p.off_ml = p.off_status + round256((size_t)(p.prefix_items + p.own_items) * 4);
     p.off_o = p.off_ml + round256((size_t)p.parts * p.rows * 8);
     p.bytes = p.off_o + round256((size_t)p.parts * p.rows * D->head_dim * 4);
     return p;
@@ -879,6 +1119,7 @@ Plan plan_of(const gdn_prefix_attn_desc *D) {
 
 template <int D>
 constexpr int tile_smem() { return (2 + kStages) * kTile * D * 2 + 1024; }
+static_assert(tile_smem<128>() + kRows * 4 + 256 <= 232448, "227 KB of shared memory a CTA, static ones included");
 
 // Raises the kernels' dynamic shared memory limits, once per device.
 template <int D>
@@ -897,34 +1138,44 @@ cudaError_t prepare_device() {
     return e;
 }
 
-// One launch over the prefix's items, the own keys' items, or both.
+// A launch that may overlap the kernel before it (see grid_wait).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(KArgs...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
+                             const Args &...args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = st;
+    cfg.attrs = &attr, cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// One launch over items [first, first + count).
 template <int D>
-cudaError_t launch_parts(PrefixParams P, const PrefixMaps &maps, const Plan &plan, bool warp, bool prefix, bool own,
+cudaError_t launch_parts(PrefixParams P, const PrefixMaps &maps, bool warp, int64_t rows, int64_t first, int64_t count,
                          cudaStream_t st) {
-    P.prefix_items = prefix ? (int32_t)plan.prefix_items : 0;
-    const int64_t items = P.prefix_items + (own ? plan.own_items : 0);
-    if (items == 0) return cudaSuccess;
-    if (!warp) {
-        gdn_tile_attn_kernel<D><<<(unsigned)items, kTThreads, tile_smem<D>(), st>>>(P, maps);
-    } else if ((prefix ? (int64_t)P.N : 1) * P.L * P.G <= 8) {
-        gdn_warp_attn_kernel<D, 1><<<(unsigned)items, kWThreads, warp_smem<D>(), st>>>(P, maps);
-    } else {
-        gdn_warp_attn_kernel<D, 2><<<(unsigned)items, kWThreads, warp_smem<D>(), st>>>(P, maps);
-    }
-    return cudaGetLastError();
+    if (count == 0) return cudaSuccess;
+    P.first_item = (int32_t)first;
+    if (!warp) return launch_dependent(gdn_tile_attn_kernel<D>, (unsigned)count, kTThreads, tile_smem<D>(), st, P, maps);
+    if (rows <= 8) return launch_dependent(gdn_warp_attn_kernel<D, 1>, (unsigned)count, kWThreads, warp_smem<D>(), st, P, maps);
+    return launch_dependent(gdn_warp_attn_kernel<D, 2>, (unsigned)count, kWThreads, warp_smem<D>(), st, P, maps);
 }
 
 template <int D>
 gdn_status launch(const PrefixParams &P, const PrefixMaps &maps, const Plan &plan, cudaStream_t st) {
     if (prepare_device<D>() != cudaSuccess) return GDN_ERR_CUDA;
-    if (plan.prefix_warp == plan.own_warp) {
-        if (launch_parts<D>(P, maps, plan, plan.own_warp, true, true, st) != cudaSuccess) return GDN_ERR_CUDA;
-    } else if (launch_parts<D>(P, maps, plan, plan.prefix_warp, true, false, st) != cudaSuccess ||
-               launch_parts<D>(P, maps, plan, plan.own_warp, false, true, st) != cudaSuccess) {
-        return GDN_ERR_CUDA;
-    }
-    gdn_attn_combine_kernel<D><<<(unsigned)((plan.rows + 7) / 8), 256, 0, st>>>(P, plan.parts);
-    return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    const int64_t own_rows = (int64_t)P.L * P.G, all_rows = P.N * own_rows;
+    const bool both = plan.prefix_warp == plan.own_warp && plan.own_items > 0;
+    cudaError_t e = cudaSuccess;
+    if (plan.prefix_items + plan.own_items == 0) e = cudaMemsetAsync(P.ws, 0, sizeof(WorkspaceHeader), st);
+    if (e == cudaSuccess)
+        e = launch_parts<D>(P, maps, plan.prefix_warp, plan.prefix_items ? all_rows : own_rows, 0,
+                            plan.prefix_items + (both ? plan.own_items : 0), st);
+    if (e == cudaSuccess && !both) e = launch_parts<D>(P, maps, plan.own_warp, own_rows, plan.prefix_items, plan.own_items, st);
+    if (e == cudaSuccess)
+        e = launch_dependent(gdn_attn_combine_kernel<D>, (unsigned)((plan.rows + 3) / 4), 128, 0, st, P, plan.parts);
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // namespace
@@ -960,19 +1211,19 @@ extern "C" gdn_status gdn_prefix_attn(const gdn_prefix_attn_desc *D, const void 
     P.out = static_cast<__nv_bfloat16 *>(out);
     P.prefix_pages = prefix_pages, P.block_table = block_table, P.seq_lens = seq_lens;
     P.ws = reinterpret_cast<WorkspaceHeader *>(ws);
-    P.nonfinite = reinterpret_cast<int32_t *>(ws + plan.off_nonfinite);
+    P.item_status = reinterpret_cast<int32_t *>(ws + plan.off_status);
     P.part_ml = reinterpret_cast<float2 *>(ws + plan.off_ml);
     P.part_o = reinterpret_cast<float *>(ws + plan.off_o);
     P.rows = plan.rows;
     P.N = D->num_seqs, P.L = D->num_tokens, P.H = D->num_heads, P.Hkv = D->num_kv_heads, P.G = P.H / P.Hkv;
     P.W = D->table_width, P.page = D->page_size, P.pages = D->num_pages, P.prefix = D->prefix_len, P.causal = D->causal;
-    P.prefix_tiles = plan.prefix_tiles, P.prefix_splits = plan.prefix_splits;
+    P.items_of_prefix = (int32_t)plan.prefix_items, P.prefix_tiles = plan.prefix_tiles, P.prefix_splits = plan.prefix_splits;
+    P.prefix_rows = plan.prefix_warp ? kWRows : kRows, P.own_rows = plan.own_warp ? kWRows : kRows;
     P.own_tiles = plan.own_tiles, P.own_splits = plan.own_splits;
     const double scale = D->scale > 0.f ? D->scale : 1.0 / std::sqrt((double)D->head_dim);
     P.scale_log2 = (float)(1.4426950408889634 * scale);
     PrefixMaps maps;
     if (!cache_map(&maps.k, k_cache, D) || !cache_map(&maps.v, v_cache, D)) return GDN_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(ws, 0, plan.off_ml, st) != cudaSuccess) return GDN_ERR_CUDA;
     return D->head_dim == 64 ? launch<64>(P, maps, plan, st) : launch<128>(P, maps, plan, st);
 }
