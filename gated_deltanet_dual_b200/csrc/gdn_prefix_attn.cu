@@ -61,7 +61,6 @@ static_assert(4 * kRegsSoftmax + kRegsOther <= 5 * kRegsLaunch, "a warpgroup wou
 constexpr int kWKeys = 64;                     // gdn_warp_attn_kernel: keys of a tile (16 per warp)
 constexpr int kWThreads = 160;                 // four warps of arithmetic and one that loads
 constexpr int kWRows = 16;                     // most query rows
-constexpr int kWStages = 3;
 constexpr int kWMinTiles = 4;                  // a split of a sequence's own keys is not shorter
 constexpr int kSms = 148;
 constexpr int kMaxSplits = 64;
@@ -654,15 +653,22 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D>
-constexpr int warp_smem() { return kWStages * 2 * kWKeys * D * 2 + 1024; }
+// Tiles on their way and CTAs that share an SM: at d = 128 and one column tile of rows three CTAs of two tiles (64
+// KB each) beat two of three, because one CTA's start lies behind two others' loads (own keys of 64
+// requests of up to 1024 tokens: 35 against 40 us); elsewhere registers allow two CTAs, or tiles are
+// small.
+template <int D, int NT>
+constexpr int warp_stages() { return D == 128 && NT == 1 ? 2 : 3; }
+template <int D, int NT>
+constexpr int warp_smem() { return warp_stages<D, NT>() * 2 * kWKeys * D * 2 + 1024; }
 
 // NT: column tiles of 8 rows.
 template <int D, int NT>
-__global__ void __launch_bounds__(kWThreads)
+__global__ void __launch_bounds__(kWThreads, D == 128 && NT == 1 ? 3 : 2)
 gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ PrefixMaps M) {
     constexpr int kHalves = D / 64;
     constexpr int kHalfBytes = kWKeys * 128;
+    constexpr int kWStages = warp_stages<D, NT>();
     constexpr int kTileBytes = kHalves * kHalfBytes;          // of K, and of V
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
@@ -694,14 +700,16 @@ gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
     }
     __syncthreads();
 
-    auto wait_ok = [&](uint64_t *bar, uint32_t parity, int where) {
-        bool ok = false;
-        for (uint32_t it = 0; it < kPWaitIters; ++it) {
-            if ((ok = mbar_try_wait(bar, parity))) break;
-            if ((it & 15) == 15 && *reinterpret_cast<volatile int *>(&s_abort)) break;
+    // Bounded wait; one that gives up marks the CTA as stopping, and every further one gives up at once: the loads
+    // stop, the other warps run through their tiles (on unspecified data).
+    auto stopped = [&] { return *reinterpret_cast<volatile int *>(&s_abort) != 0; };
+    auto wait = [&](uint64_t *bar, uint32_t parity, int where) {
+        if (mbar_try_wait(bar, parity)) return;
+        for (uint32_t it = 0; it < kPWaitIters / 16; ++it) {
+            if (mbar_wait_some(bar, parity)) return;
+            if (stopped()) return;
         }
-        if (!ok && atomicExch(&s_abort, 1) == 0) atomicExch(&s_status, (int)GDN_ERR_TIMEOUT | where << 16);
-        return __all_sync(0xffffffffu, ok) != 0;
+        if (atomicExch(&s_abort, 1) == 0) atomicOr(&s_status, (int)GDN_ERR_TIMEOUT | where << 16);
     };
 
     float acc[D / 16][NT][4];                  // O^T: (d, row)
@@ -731,7 +739,11 @@ gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
                 if (id >= 0 && id < P.pages) row = id * P.page + key % P.page;
                 else atomicOr(&s_status, (int)GDN_ERR_INVALID_ARG);
             }
-            if (issued >= kWStages && !wait_ok(&empty[slot], (issued / kWStages - 1) & 1, 11)) break;
+            if (issued >= kWStages) {
+                wait(&empty[slot], (issued / kWStages - 1) & 1, 11);
+                __syncwarp();
+                if (__any_sync(0xffffffffu, stopped())) break;     // the slot may still be in use
+            }
             if (lane == 0) mbar_arrive_expect_tx(&full[slot], 2 * kTileBytes);
             __syncwarp();
             if (mine)
@@ -739,7 +751,7 @@ gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
                             value ? &M.v : &M.k, &full[slot], half * 64, w.hk, row);
             __syncwarp();
         }
-        if (issued < tiles && lane == 0)       // gave up: the loads in flight still land
+        if (__any_sync(0xffffffffu, stopped()) && lane == 0)       // gave up: the loads in flight still land
             for (int i = max(0, issued - kWStages); i < issued; ++i)
                 mbar_wait(&full[i % kWStages], (i / kWStages) & 1, kDrainWaitIters);
     } else {
@@ -762,13 +774,15 @@ gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
             }
         }
         const float sl2 = P.scale_log2;
+        const int newest = (w.n >= 0 && P.causal) ? w.keys - (P.L - 1) : w.keys;     // keys before it are for every row
         // ldmatrix addresses inside this warp's 16 rows: K (row, 8 columns), V transposed
         const int krow = warp * 16 + (lane & 15), kchunk = lane >> 4;
         const int vrow = warp * 16 + (lane & 7) + ((lane >> 4) & 1) * 8, vchunk = (lane >> 3) & 1;
         const uint32_t smb = smem_u32(sm);
         for (int i = 0; i < tiles; ++i) {
             const int slot = i % kWStages;
-            if (!wait_ok(&full[slot], (i / kWStages) & 1, 12)) break;
+            wait(&full[slot], (i / kWStages) & 1, 12);
+            __syncwarp();
             const int key0 = (w.t0 + i) * kWKeys + warp * 16;      // this warp's keys [key0, key0 + 16)
             if (key0 < w.keys) {
                 const uint32_t kb = smb + 2 * slot * kTileBytes, vb = kb + kTileBytes;
@@ -782,10 +796,14 @@ gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
 #pragma unroll
                     for (int n = 0; n < NT; ++n) mma16816(s[n], a, qf[kk][n][0], qf[kk][n][1]);
                 }
-                // V rows that a row of the tile must not see (see the file comment)
                 const int last = min(16, w.keys - key0);
-                const int newest = (w.n >= 0 && P.causal) ? w.keys - (P.L - 1) : w.keys;
-                if (last < 16 || newest < key0 + last) {
+                if (last < 16 || newest < key0 + 16) {             // not every key is for every row
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (key0 + (lane >> 2) + (e >> 1) * 8 >= sees[n][e & 1]) s[n][e] = -INFINITY;
+                    // nor is every V row (see the file comment)
                     uint8_t *v = sm + (2 * slot + 1) * kTileBytes;
                     bool found = false;
                     for (int x = lane; x < 16 * (D / 8); x += 32) {
@@ -811,34 +829,42 @@ gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
                     fence_async_smem();        // before the slot's next load
                     __syncwarp();
                 }
+                // The reference max moves only when a score passes it by more than the margin: a vote, and
+                // the rows' maxima across lanes only then
+                bool up = false;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) up = up || s[n][e] * sl2 > m_ref[n][e & 1] + kMargin;
+                if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float mt = fmaxf(s[n][e], s[n][e + 2]) * sl2;
+                            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
+                            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
+                            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+                            if (mt > m_ref[n][e] + kMargin) {
+                                const float alpha = m_ref[n][e] == -INFINITY ? 0.f : ex2_approx(m_ref[n][e] - mt);
+                                m_ref[n][e] = mt;
+                                l_sum[n][e] *= alpha;
+#pragma unroll
+                                for (int d0 = 0; d0 < D / 16; ++d0) {
+                                    acc[d0][n][e] *= alpha;
+                                    acc[d0][n][e + 2] *= alpha;
+                                }
+                            }
+                        }
+                }
                 uint32_t pf[NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = key0 + (lane >> 2) + (e >> 1) * 8;
-                        s[n][e] = key < sees[n][e & 1] ? s[n][e] * sl2 : -INFINITY;
-                    }
-#pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mt = fmaxf(s[n][e], s[n][e + 2]);
-                        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
-                        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
-                        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-                        const bool up = mt > m_ref[n][e] + kMargin;
-                        if (__any_sync(0xffffffffu, up)) {
-                            const float alpha = !up ? 1.f : m_ref[n][e] == -INFINITY ? 0.f : ex2_approx(m_ref[n][e] - mt);
-                            if (up) m_ref[n][e] = mt;
-                            l_sum[n][e] *= alpha;
-#pragma unroll
-                            for (int d0 = 0; d0 < D / 16; ++d0) {
-                                acc[d0][n][e] *= alpha;
-                                acc[d0][n][e + 2] *= alpha;
-                            }
-                        }
                         const float mu = m_ref[n][e] == -INFINITY ? 0.f : m_ref[n][e];
-                        s[n][e] = ex2_approx(s[n][e] - mu);
-                        s[n][e + 2] = ex2_approx(s[n][e + 2] - mu);
+                        s[n][e] = ex2_approx(fmaf(s[n][e], sl2, -mu));
+                        s[n][e + 2] = ex2_approx(fmaf(s[n][e + 2], sl2, -mu));
                         l_sum[n][e] += s[n][e] + s[n][e + 2];
                     }
                     pf[n][0] = transpose8x8(pack_bf2(s[n][0], s[n][1]));
@@ -1084,11 +1110,11 @@ int best_split(int64_t base, int64_t tiles) {
     return best;
 }
 
-// The same for gdn_warp_attn_kernel, whose CTAs share an SM and whose lists differ in length: four
-// CTAs for each place on the GPU while no split gets shorter than its least.
+// The same for gdn_warp_attn_kernel, whose CTAs share an SM and whose lists differ in length: about
+// three CTAs for each place on the GPU while no split gets shorter than its least.
 int warp_split(int64_t base, int64_t keys) {
     const int64_t most = (keys + kWKeys * kWMinTiles - 1) / (kWKeys * kWMinTiles);
-    return (int)std::max<int64_t>(1, std::min<int64_t>({(4 * 2 * kSms + base - 1) / base, most, kMaxSplits}));
+    return (int)std::max<int64_t>(1, std::min<int64_t>({(8 * kSms + base - 1) / base, most, kMaxSplits}));
 }
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -1132,8 +1158,8 @@ cudaError_t prepare_device() {
     if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
     constexpr auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
     e = cudaFuncSetAttribute(gdn_tile_attn_kernel<D>, attr, tile_smem<D>());
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_warp_attn_kernel<D, 1>, attr, warp_smem<D>());
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_warp_attn_kernel<D, 2>, attr, warp_smem<D>());
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_warp_attn_kernel<D, 1>, attr, warp_smem<D, 1>());
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_warp_attn_kernel<D, 2>, attr, warp_smem<D, 2>());
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
     return e;
 }
@@ -1158,8 +1184,8 @@ cudaError_t launch_parts(PrefixParams P, const PrefixMaps &maps, bool warp, int6
     if (count == 0) return cudaSuccess;
     P.first_item = (int32_t)first;
     if (!warp) return launch_dependent(gdn_tile_attn_kernel<D>, (unsigned)count, kTThreads, tile_smem<D>(), st, P, maps);
-    if (rows <= 8) return launch_dependent(gdn_warp_attn_kernel<D, 1>, (unsigned)count, kWThreads, warp_smem<D>(), st, P, maps);
-    return launch_dependent(gdn_warp_attn_kernel<D, 2>, (unsigned)count, kWThreads, warp_smem<D>(), st, P, maps);
+    if (rows <= 8) return launch_dependent(gdn_warp_attn_kernel<D, 1>, (unsigned)count, kWThreads, warp_smem<D, 1>(), st, P, maps);
+    return launch_dependent(gdn_warp_attn_kernel<D, 2>, (unsigned)count, kWThreads, warp_smem<D, 2>(), st, P, maps);
 }
 
 template <int D>
