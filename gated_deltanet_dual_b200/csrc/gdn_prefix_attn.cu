@@ -106,6 +106,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         : "memory");
 }
 
+// 16 bytes global -> shared, asynchronously; zeros where !in (nothing is read).
+__device__ __forceinline__ void cp_async16_or_zero(void *dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
 // One lane of a converged warp, the same one each time.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
@@ -288,26 +293,36 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
     // The ring's order is the order of use: K0 K1 V0 K2 V1 ... V(last).  Loads tile i of the ring (warp 16):
     // lane = (half, box), a box is min(p, 64) rows of one page, 64 columns; rows past the end read as zeros.
     auto v_at = [&](int j) { return j + 1 < tiles ? 2 * j + 2 : 2 * j + 1; };
+    const int box_rows = min(P.page, 64), boxes = kTile / box_rows, box = lane % boxes, half_of = lane / boxes;
+    // This lane's cache row in key tile j, for K and again for V; the page ids of the tile after are on their way.
+    int id_next = -1, rows_of[2] = {0, 0};
+    auto fetch_id = [&](int j) {
+        const int key = (w.t0 + j) * kTile + box * box_rows;
+        id_next = half_of < kHalves && j < tiles && key < w.keys ? w.list[key / P.page] : -2;
+    };
     auto load = [&](int i) {
-        const int box_rows = min(P.page, 64), boxes = kTile / box_rows;
-        const int box = lane % boxes, half = lane / boxes;
         const bool value = i > 0 && ((i & 1) == 0 || i == 2 * tiles - 1);
-        const int j = w.t0 + (value ? (i == 2 * tiles - 1 ? tiles - 1 : i / 2 - 1) : (i + 1) / 2);
-        const int slot = i % kStages, key = j * kTile + box * box_rows;
-        int row = P.pages * P.page;
-        if (half < kHalves && key < w.keys) {
-            const int id = w.list[key / P.page];
-            if (id >= 0 && id < P.pages) row = id * P.page + key % P.page;
-            else atomicOr(&s_status, (int)GDN_ERR_INVALID_ARG);
+        const int j = value ? (i == 2 * tiles - 1 ? tiles - 1 : i / 2 - 1) : (i + 1) / 2;
+        const int slot = i % kStages;
+        if (!value) {
+            const int id = id_next;
+            int row = P.pages * P.page;        // past the end: reads as zeros
+            if (id >= 0 && id < P.pages) row = id * P.page + ((w.t0 + j) * kTile + box * box_rows) % P.page;
+            else if (id != -2) atomicOr(&s_status, (int)GDN_ERR_INVALID_ARG);
+            if (j & 1) rows_of[1] = row;
+            else rows_of[0] = row;
+            fetch_id(j + 1);
         }
+        const int row = j & 1 ? rows_of[1] : rows_of[0];
         if (lane == 0) mbar_arrive_expect_tx(&full[slot], kTileBytes);
         __syncwarp();
-        if (half < kHalves)
-            tma_load_3d(sm_kv + slot * kTileBytes + half * (kTile * 128) + box * box_rows * 128, value ? &M.v : &M.k,
-                        &full[slot], half * 64, w.hk, row);
+        if (half_of < kHalves)
+            tma_load_3d(sm_kv + slot * kTileBytes + half_of * (kTile * 128) + box * box_rows * 128, value ? &M.v : &M.k,
+                        &full[slot], half_of * 64, w.hk, row);
         __syncwarp();
     };
     if (warp == 16) {
+        fetch_id(0);
         if (lane == 0) {
             for (int i = 0; i < kStages; ++i) {
                 mbar_init(&full[i], 1);
@@ -331,27 +346,24 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
         tmem_alloc(&s_tmem, 512);
         tmem_relinquish();
     } else if (warp < 16) {
-        // queries: D / 8 chunks of 16 bytes a row, a pass covers 512 / (D / 8) rows; all loads ahead of the stores
-        constexpr int kChunks = D / 8, kPass = 512 / kChunks, kBatch = kTile / kPass;
-        const int c = tid % kChunks, r0 = tid / kChunks;
-        int nl = (w.row0 + r0) / P.G, g = (w.row0 + r0) - nl * P.G;       // (n, l) and head of the row
+        // queries: D / 8 chunks of 16 bytes a row, a pass covers 512 / (D / 8) rows; asynchronous copies in a short
+        // loop (a launch starts with cold instruction caches); rows past the last are zeros
+        constexpr int kChunks = D / 8, kPass = 512 / kChunks;
+        const int c = tid % kChunks;
+        int r = tid / kChunks;
+        int nl = (w.row0 + r) / P.G, g = (w.row0 + r) - nl * P.G;         // (n, l) and head of the row
         const int dn = kPass / P.G, dg = kPass - dn * P.G;               // the same of kPass rows
         const __nv_bfloat16 *head = P.q + (int64_t)w.hk * P.G * D + c * 8;
+        uint8_t *dst = sm_q + (c >> 3) * (kTile * 128) + sw128_off(r, c & 7);
 #pragma unroll 1
-        for (int t = 0; t <= two; ++t) {
-            uint4 u[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                u[i] = make_uint4(0, 0, 0, 0);
-                if (t * kTile + r0 + i * kPass < w.nrows)
-                    u[i] = *reinterpret_cast<const uint4 *>(head + ((int64_t)nl * P.H + g) * D);
-                nl += dn;
-                if ((g += dg) >= P.G) g -= P.G, ++nl;
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                *reinterpret_cast<uint4 *>(sm_q + t * kTileBytes + (c >> 3) * (kTile * 128) + sw128_off(r0 + i * kPass, c & 7)) = u[i];
+        for (int i = 0; i < (1 + two) * kTile / kPass; ++i) {
+            const bool in = r < w.nrows;
+            cp_async16_or_zero(dst + (r >> 7) * (kTileBytes - kTile * 128), head + (in ? ((int64_t)nl * P.H + g) * D : 0), in);
+            r += kPass, dst += kPass * 128, nl += dn;
+            if ((g += dg) >= P.G) g -= P.G, ++nl;
         }
+        cp_async_commit();
+        cp_async_wait_all();
         fence_async_smem();
     }
     tc_fence_before();
@@ -545,8 +557,19 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
                     // P = 2^(s - m) with the reference max of the tiles before, while the tile's own max is
                     // taken beside it (it would wait for itself in a pass of its own).  Only if that max
                     // passes the reference by more than the margin is m moved, O and l rescaled and P taken
-                    // again: in a list's first tile, and rarely later.  The rows' two warps decide together.
+                    // again, which is rare.  The rows' two warps decide together.
                     float ls;
+                    if (j == 0) {              // no reference yet: the row's max first, through its two threads
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int e = 0; e < 64; e += 2) mx[e / 2 & 3] = fmaxf(mx[e / 2 & 3], fmaxf(x[e / 32][e % 32], x[e / 32][e % 32 + 1]));
+                        float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                        if (half == 0) s_pair[r] = mt;
+                        asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+                        if (half == 1) s_pair[r] = mt = fmaxf(mt, s_pair[r]);
+                        asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+                        m_ref = s_pair[r];
+                    }
                     while (true) {
                         float mt;
                         softmax_half(x, sl2, m_ref, tp, ls, mt, free);
