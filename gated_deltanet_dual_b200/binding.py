@@ -645,12 +645,83 @@ def backward_conv_workspace_size(desc: Desc, doc_offsets) -> int:
     return int(fn(ctypes.byref(desc), offs.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))))
 
 
+# ----------------------------------------------------------------------------- serving calls
+# The calls below are made once per layer and decode step, so their checks are kept short: one comparison
+# per property, and the full message only on the way to an exception.
+def _want(t: torch.Tensor, name: str, shape, dtype, index: int):
+    """t is a contiguous CUDA tensor of this shape and dtype on device `index`, or raises."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _check(t, name, shape, dtype, torch.device("cuda", index))
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+
+
+def _rows(t: Optional[torch.Tensor], name: str, shape, dtype, index: int):
+    """(row stride, head stride) in elements of [..., rows, heads, d] with contiguous heads."""
+    if t is None:
+        return 0, 0
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype} != {dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    if len(shape) == 4 and shape[0] > 1 and st[0] != shape[1] * st[1]:
+        raise ValueError(f"{name}: the views must lie {shape[1]} rows apart")
+    return st[-3], st[-2]
+
+
+def _cuda_index(t: torch.Tensor) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("inputs must be CUDA tensors")
+    return index
+
+
+def _raw_stream(index: int, stream) -> int:
+    """The given stream, or the current one of device `index`."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream
+
+
+def _call(name: str, index: int, stream, fresh, *args):
+    """Calls the library on device `index` and raises on an error.  Tensors that the caller allocated itself
+    (fresh) are kept alive for a stream that is not the current one."""
+    fn = getattr(load_library(), name)
+    if torch.cuda.current_device() == index:
+        st = fn(*args, _raw_stream(index, stream))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index, stream))
+    if stream is not None:
+        other = torch.cuda.ExternalStream(stream, device=index)
+        for t in fresh:
+            if t is not None:
+                t.record_stream(other)
+    if st != GDN_OK:
+        raise GdnError(st, f"{name} failed: {status_string(st)}")
+
+
 # ----------------------------------------------------------------------------- rotary positions
 class RotaryTable:
     """The frequencies of a rotary embedding on the device (made by rotary_table, kept by the caller)."""
 
     def __init__(self, turns: torch.Tensor, rot_dim: int, interleaved: bool, scale: float):
-        self.turns, self.rot_dim, self.interleaved, self.scale = turns, rot_dim, bool(interleaved), float(scale)
+        if turns.dtype != torch.int64 or tuple(turns.shape) != (rot_dim // 2,) or not turns.is_contiguous():
+            raise ValueError("turns must be a contiguous int64 tensor of rot_dim / 2 entries")
+        self._turns, self._index, self._ptr = turns, turns.get_device(), turns.data_ptr()
+        self._args = int(rot_dim), int(bool(interleaved)), float(scale)
+
+    turns = property(lambda self: self._turns)
+    rot_dim = property(lambda self: self._args[0])
+    interleaved = property(lambda self: bool(self._args[1]))
+    scale = property(lambda self: self._args[2])
+
+    def _on(self, index: int):
+        if self._index != index:
+            raise ValueError(f"the rotary table is on {self._turns.device}, expected cuda:{index}")
+        return self._ptr
 
 
 def rotary_frequencies(rot_dim, *, base=10000.0, scaling="none", factor=1.0, original_len=0, beta_fast=32.0,
@@ -678,92 +749,34 @@ def rotary_table(rot_dim, *, interleaved=False, base=10000.0, scaling="none", fa
     return RotaryTable(torch.from_numpy(turns.view(np.int64).copy()).to(device), int(rot_dim), interleaved, attn_scale)
 
 
-def _i32(t: torch.Tensor, name: str, shape, device):
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
-        _check(t, name, shape, torch.int32, device)
-
-
-def _rows(t: Optional[torch.Tensor], name: str, shape, dtype, device):
-    """(row stride, head stride) in elements of [..., rows, heads, d] with contiguous heads."""
-    if t is None:
-        return 0, 0
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} != {shape}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: dtype {t.dtype} != {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    st = t.stride()
-    if shape[-1] > 1 and st[-1] != 1:
-        raise ValueError(f"{name}: the elements of a head must be contiguous")
-    if len(shape) == 4 and shape[0] > 1 and st[0] != shape[1] * st[1]:
-        raise ValueError(f"{name}: the views must lie {shape[1]} rows apart")
-    return st[-3], st[-2]
-
-
-class _On:
-    """Runs a call on the tensors' device: its current stream unless one is given.  Tensors that the call
-    allocated itself are kept alive for a stream other than the current one."""
-
-    def __init__(self, device, stream):
-        self.device, self.given = device, stream
-        self.guard = None
-
-    def __enter__(self):
-        if torch.cuda.current_device() != self.device.index:
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        self.stream = torch.cuda.current_stream(self.device).cuda_stream if self.given is None else self.given
-        return self
-
-    def keep(self, *tensors):
-        if self.given is not None:
-            other = torch.cuda.ExternalStream(self.given, device=self.device)
-            for t in tensors:
-                t.record_stream(other)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
 def _rotary(name, q, k, positions, table, q_out, k_out, stream):
     lead = q if q is not None else k
     if lead is None:
         raise ValueError("q and k are both None")
-    dev, io = lead.device, lead.dtype
-    if dev.type != "cuda":
-        raise ValueError("inputs must be CUDA tensors")
+    index, io = _cuda_index(lead), lead.dtype
     if lead.ndim not in (3, 4):
         raise ValueError("q and k must be [T, H, d] or [V, T, H, d]")
-    front, d = tuple(lead.shape[:-2]), lead.shape[-1]
+    front, d = lead.shape[:-2], lead.shape[-1]
     T = front[-1]
     H = q.shape[-2] if q is not None else 0
     Hkv = k.shape[-2] if k is not None else 0
     rows = T * (front[0] if len(front) == 2 else 1)
     fresh = []
     if q is not None and q_out is None:
-        q_out = torch.empty(front + (H, d), dtype=io, device=dev)
+        q_out = torch.empty(front + (H, d), dtype=io, device=lead.device)
         fresh.append(q_out)
     if k is not None and k_out is None:
-        k_out = torch.empty(front + (Hkv, d), dtype=io, device=dev)
+        k_out = torch.empty(front + (Hkv, d), dtype=io, device=lead.device)
         fresh.append(k_out)
-    strides = (_rows(q, "q", front + (H, d), io, dev) + _rows(k, "k", front + (Hkv, d), io, dev)
-               + _rows(q_out if q is not None else None, "q_out", front + (H, d), io, dev)
-               + _rows(k_out if k is not None else None, "k_out", front + (Hkv, d), io, dev))
-    _i32(positions, "positions", (T,), dev)
-    _check(table.turns, "table.turns", (table.rot_dim // 2,), torch.int64, dev)
+    strides = (_rows(q, "q", front + (H, d), io, index) + _rows(k, "k", front + (Hkv, d), io, index)
+               + _rows(q_out if q is not None else None, "q_out", front + (H, d), io, index)
+               + _rows(k_out if k is not None else None, "k_out", front + (Hkv, d), io, index))
+    _want(positions, "positions", (T,), torch.int32, index)
+    turns = table._on(index)
     if rows and H + Hkv:
-        desc = RotaryDesc(rows, T, H, Hkv, d, table.rot_dim, int(table.interleaved), _dtype_code(lead), table.scale, 0,
-                          *strides)
-        with _On(dev, stream) as on:
-            st = getattr(load_library(), name)(ctypes.byref(desc), table.turns.data_ptr(), positions.data_ptr(),
-                                               q.data_ptr() if H else None, k.data_ptr() if Hkv else None,
-                                               q_out.data_ptr() if H else None, k_out.data_ptr() if Hkv else None,
-                                               on.stream)
-            on.keep(*fresh)
-        if st != GDN_OK:
-            raise GdnError(st, f"{name} failed: {status_string(st)}")
+        desc = RotaryDesc(rows, T, H, Hkv, d, table._args[0], table._args[1], _dtype_code(lead), table._args[2], 0, *strides)
+        _call(name, index, stream, fresh, ctypes.byref(desc), turns, positions.data_ptr(), q.data_ptr() if H else None,
+              k.data_ptr() if Hkv else None, q_out.data_ptr() if H else None, k_out.data_ptr() if Hkv else None)
     return q_out if q is not None else None, k_out if k is not None else None
 
 
@@ -782,12 +795,20 @@ def rotary_backward(dq, dk, positions, table: RotaryTable, *, dq_out=None, dk_ou
 # ----------------------------------------------------------------------------- paged key/value cache
 class KvTables:
     """What kv_extend writes for a step of num_seqs sequences and at most max_new_tokens packed rows:
-    slot_map, positions [max_new_tokens], cu_new [num_seqs + 1], seq_lens [num_seqs], free_left [1]."""
+    slot_map, positions [max_new_tokens], cu_new [num_seqs + 1], seq_lens [num_seqs], free_left [1], all int32."""
 
     def __init__(self, num_seqs: int, max_new_tokens: int, device="cuda"):
-        empty = lambda n: torch.empty(n, dtype=torch.int32, device=device)
-        self.slot_map, self.positions, self.cu_new = empty(max_new_tokens), empty(max_new_tokens), empty(num_seqs + 1)
-        self.seq_lens, self.free_left = empty(num_seqs), empty(1)
+        sizes = (max_new_tokens, max_new_tokens, num_seqs + 1, num_seqs, 1)
+        self._tensors = tuple(torch.empty(n, dtype=torch.int32, device=device) for n in sizes)
+        self._index = self._tensors[4].get_device()
+        self._sizes = int(num_seqs), int(max_new_tokens)
+        self._ptrs = tuple(t.data_ptr() if t.numel() else None for t in self._tensors)
+
+    slot_map = property(lambda self: self._tensors[0])
+    positions = property(lambda self: self._tensors[1])
+    cu_new = property(lambda self: self._tensors[2])
+    seq_lens = property(lambda self: self._tensors[3])
+    free_left = property(lambda self: self._tensors[4])
 
 
 def kv_extend(block_table, seq_lens, new_lens, free_pages, free_count, page_size, tables: KvTables, *, prefix_len=0,
@@ -796,31 +817,24 @@ def kv_extend(block_table, seq_lens, new_lens, free_pages, free_count, page_size
     extended in place with pages from the top of free_pages [F] (free_count [1] of them are free),
     tables receives the rest.  The next step takes tables.seq_lens and tables.free_left as its
     seq_lens and free_count (from another KvTables: outputs must not overlap inputs)."""
-    dev = block_table.device
-    if dev.type != "cuda":
-        raise ValueError("inputs must be CUDA tensors")
+    index, i32 = _cuda_index(block_table), torch.int32
     if block_table.ndim != 2:
         raise ValueError("block_table must be [N, W]")
     N, W = block_table.shape
-    F, M = free_pages.numel(), tables.slot_map.numel()
-    for t, name, shape in ((block_table, "block_table", (N, W)), (seq_lens, "seq_lens", (N,)), (new_lens, "new_lens", (N,)),
-                           (free_pages, "free_pages", (F,)), (free_count, "free_count", (1,)),
-                           (tables.slot_map, "slot_map", (M,)), (tables.positions, "positions", (M,)),
-                           (tables.cu_new, "cu_new", (N + 1,)), (tables.seq_lens, "tables.seq_lens", (N,)),
-                           (tables.free_left, "free_left", (1,))):
-        _i32(t, name, shape, dev)
+    F, M = free_pages.numel(), tables._sizes[1]
+    _want(block_table, "block_table", (N, W), i32, index)
+    _want(seq_lens, "seq_lens", (N,), i32, index)
+    _want(new_lens, "new_lens", (N,), i32, index)
+    _want(free_pages, "free_pages", (F,), i32, index)
+    _want(free_count, "free_count", (1,), i32, index)
+    if tables._sizes[0] != N or tables._index != index:
+        raise ValueError(f"tables are made for {tables._sizes[0]} sequences on {tables.free_left.device}, not for {N} on cuda:{index}")
     if device_status is not None:
-        _i32(device_status, "device_status", (1,), dev)
-    desc = KvExtendDesc(N, W, int(page_size), F, M, int(prefix_len), 0, 0)
-    with _On(dev, stream) as on:
-        st = load_library().gdn_kv_extend(ctypes.byref(desc), block_table.data_ptr(), seq_lens.data_ptr(),
-                                          new_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
-                                          tables.slot_map.data_ptr(), tables.positions.data_ptr(),
-                                          tables.cu_new.data_ptr(), tables.seq_lens.data_ptr(),
-                                          tables.free_left.data_ptr(),
-                                          None if device_status is None else device_status.data_ptr(), on.stream)
-    if st != GDN_OK:
-        raise GdnError(st, f"gdn_kv_extend failed: {status_string(st)}")
+        _want(device_status, "device_status", (1,), i32, index)
+    desc = KvExtendDesc(N, W, page_size, F, M, prefix_len, 0, 0)
+    _call("gdn_kv_extend", index, stream, (), ctypes.byref(desc), block_table.data_ptr(), seq_lens.data_ptr(),
+          new_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), *tables._ptrs,
+          None if device_status is None else device_status.data_ptr())
     return tables
 
 
@@ -829,42 +843,34 @@ def rotary_append(q, k, v, positions, slot_map, table: RotaryTable, k_cache, v_c
     """Rotary positions fused with the append to the cache (gdn_rotary_append): q [R, H, d] rotated into
     q_out, k [R, H_kv, d] rotated into k_cache [P, p, H_kv, d] and v copied into v_cache, at slot_map [R]
     int32.  Rows with slot -1 are padding and are left as they were.  Returns q_out."""
-    dev, io = q.device, q.dtype
-    if dev.type != "cuda":
-        raise ValueError("inputs must be CUDA tensors")
+    index, io = _cuda_index(q), q.dtype
     if q.ndim != 3 or k.ndim != 3 or k_cache.ndim != 4:
         raise ValueError("q, k and v must be [R, heads, d] and the caches [P, p, H_kv, d]")
     R, H, d = q.shape
     Hkv, (P, page) = k.shape[1], k_cache.shape[:2]
-    fresh = q_out is None
-    if fresh:
-        q_out = torch.empty(R, H, d, dtype=io, device=dev)
-    strides = (_rows(q, "q", (R, H, d), io, dev) + _rows(k, "k", (R, Hkv, d), io, dev)
-               + _rows(v, "v", (R, Hkv, d), io, dev) + _rows(q_out, "q_out", (R, H, d), io, dev))
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _check(t, name, (P, page, Hkv, d), io, dev)
-    _i32(positions, "positions", (R,), dev)
-    _i32(slot_map, "slot_map", (R,), dev)
+    fresh = ()
+    if q_out is None:
+        q_out = torch.empty(R, H, d, dtype=io, device=q.device)
+        fresh = (q_out,)
+    strides = (_rows(q, "q", (R, H, d), io, index) + _rows(k, "k", (R, Hkv, d), io, index)
+               + _rows(v, "v", (R, Hkv, d), io, index) + _rows(q_out, "q_out", (R, H, d), io, index))
+    _want(k_cache, "k_cache", (P, page, Hkv, d), io, index)
+    _want(v_cache, "v_cache", (P, page, Hkv, d), io, index)
+    _want(positions, "positions", (R,), torch.int32, index)
+    _want(slot_map, "slot_map", (R,), torch.int32, index)
     if device_status is not None:
-        _i32(device_status, "device_status", (1,), dev)
-    _check(table.turns, "table.turns", (table.rot_dim // 2,), torch.int64, dev)
-    desc = AppendDesc(R, H, Hkv, d, table.rot_dim, int(table.interleaved), page, P, _dtype_code(q), table.scale, *strides)
-    with _On(dev, stream) as on:
-        st = load_library().gdn_rotary_append(ctypes.byref(desc), table.turns.data_ptr(), positions.data_ptr(),
-                                              slot_map.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                              q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                              None if device_status is None else device_status.data_ptr(), on.stream)
-        if fresh:
-            on.keep(q_out)
-    if st != GDN_OK:
-        raise GdnError(st, f"gdn_rotary_append failed: {status_string(st)}")
+        _want(device_status, "device_status", (1,), torch.int32, index)
+    desc = AppendDesc(R, H, Hkv, d, table._args[0], table._args[1], page, P, _dtype_code(q), table._args[2], *strides)
+    _call("gdn_rotary_append", index, stream, fresh, ctypes.byref(desc), table._on(index), positions.data_ptr(),
+          slot_map.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), None if device_status is None else device_status.data_ptr())
     return q_out
 
 
 def make_prefix_attn_desc(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, page_size, num_pages, table_width,
                           prefix_len, causal, scale=None, dtype_code=GDN_BF16) -> PrefixAttnDesc:
     return PrefixAttnDesc(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, page_size, num_pages, table_width,
-                          prefix_len, int(bool(causal)), dtype_code, 0.0 if scale is None else float(scale))
+                          prefix_len, 1 if causal else 0, dtype_code, 0.0 if scale is None else scale)
 
 
 def prefix_attn_workspace_size(desc: PrefixAttnDesc) -> int:
@@ -878,47 +884,39 @@ def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len, block_table,
     first prefix_len tokens on the pages prefix_pages) and each sequence's own seq_lens[n] keys through
     block_table [N, W], in caches [P, p, H_kv, d] (gdn_prefix_attn).  causal=False lets the L tokens see
     one another (a denoised block).  Returns out [N, L, H, d]."""
-    dev, bf = q.device, q.dtype
-    if dev.type != "cuda":
-        raise ValueError("inputs must be CUDA tensors")
+    index, io = _cuda_index(q), q.dtype
     if q.ndim != 4 or k_cache.ndim != 4 or block_table.ndim != 2:
         raise ValueError("q must be [N, L, H, d], the caches [P, p, H_kv, d] and block_table [N, W]")
-    N, L, H, d = q.shape
+    N, L, H, d = shape = q.shape
     P, page, Hkv = k_cache.shape[:3]
     W = block_table.shape[1]
-    _check(q, "q", (N, L, H, d), bf, dev)
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _check(t, name, (P, page, Hkv, d), bf, dev)
-    _i32(block_table, "block_table", (N, W), dev)
-    _i32(seq_lens, "seq_lens", (N,), dev)
+    cache = (P, page, Hkv, d)
+    _want(q, "q", shape, io, index)
+    _want(k_cache, "k_cache", cache, io, index)
+    _want(v_cache, "v_cache", cache, io, index)
+    _want(block_table, "block_table", (N, W), torch.int32, index)
+    _want(seq_lens, "seq_lens", (N,), torch.int32, index)
     if scale is not None and not scale > 0:
         raise ValueError("scale must be positive")
-    prefix_len = int(prefix_len)
     if prefix_len:
-        _i32(prefix_pages, "prefix_pages", (prefix_pages.numel(),), dev)
+        _want(prefix_pages, "prefix_pages", (prefix_pages.numel(),), torch.int32, index)
         if prefix_len < 0 or prefix_pages.numel() < -(-prefix_len // page):
             raise ValueError(f"prefix_pages holds {prefix_pages.numel()} pages of {page} for {prefix_len} tokens")
-    fresh = []
+    fresh = ()
     if out is None:
-        out = torch.empty(N, L, H, d, dtype=bf, device=dev)
-        fresh.append(out)
+        out = torch.empty(shape, dtype=io, device=q.device)
+        fresh = (out,)
     else:
-        _check(out, "out", (N, L, H, d), bf, dev)
+        _want(out, "out", shape, io, index)
     desc = make_prefix_attn_desc(N, L, H, Hkv, d, page, P, W, prefix_len, causal, scale, _dtype_code(q))
-    lib = load_library()
     if workspace is None:
-        nbytes = int(lib.gdn_prefix_attn_workspace_size(ctypes.byref(desc)))
-        ws = torch.empty(max(256, nbytes), dtype=torch.uint8, device=dev)
-        fresh.append(ws)
+        ws = torch.empty(max(256, prefix_attn_workspace_size(desc)), dtype=torch.uint8, device=q.device)
+        fresh += (ws,)
     else:
         ws = workspace.tensor
-        if ws.device != dev:
-            raise ValueError(f"workspace is on {ws.device}, expected {dev}")
-    with _On(dev, stream) as on:
-        st = lib.gdn_prefix_attn(ctypes.byref(desc), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                 prefix_pages.data_ptr() if prefix_len else None, block_table.data_ptr() if W else None,
-                                 seq_lens.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(), on.stream)
-        on.keep(*fresh)
-    if st != GDN_OK:
-        raise GdnError(st, f"gdn_prefix_attn failed: {status_string(st)}")
+        if ws.get_device() != index:
+            raise ValueError(f"workspace is on {ws.device}, expected cuda:{index}")
+    _call("gdn_prefix_attn", index, stream, fresh, ctypes.byref(desc), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          prefix_pages.data_ptr() if prefix_len else None, block_table.data_ptr() if W else None, seq_lens.data_ptr(),
+          out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
