@@ -904,11 +904,12 @@ def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len, block_table,
             raise ValueError(f"prefix_pages holds {prefix_pages.numel()} pages of {page} for {prefix_len} tokens")
     fresh = ()
     if out is None:
-        out = torch.empty(shape, dtype=io, device=q.device)
+        out = torch.empty_like(q)
         fresh = (out,)
     else:
         _want(out, "out", shape, io, index)
-    desc = make_prefix_attn_desc(N, L, H, Hkv, d, page, P, W, prefix_len, causal, scale, _dtype_code(q))
+    desc = PrefixAttnDesc(N, L, H, Hkv, d, page, P, W, prefix_len, 1 if causal else 0, _dtype_code(q),
+                          0.0 if scale is None else scale)
     if workspace is None:
         ws = torch.empty(max(256, prefix_attn_workspace_size(desc)), dtype=torch.uint8, device=q.device)
         fresh += (ws,)

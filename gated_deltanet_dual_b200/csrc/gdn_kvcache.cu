@@ -1,13 +1,12 @@
 // gdn_kvcache.cu -- block tables, slots and positions of a serving step's new tokens
 // (gdn_kv_extend of include/gdn_kvcache.h).
 //
-// Two exclusive sums over the sequences -- pages needed and tokens -- decide everything: which
-// entry of the free list a new page takes and which packed row a token has.  A few kilobytes are
-// read and 8 bytes per token written, so the call is bound by latency: one launch, in which every
-// CTA runs the whole scan itself (4096 sequences per pass of 1024 threads; the lengths come from
-// L2) and then writes only its own range of token rows.  A token whose index starts a page also
-// writes that page's table entry, so entries have one writer and no CTA reads an entry that
-// another one writes (rows on new pages take the page from the free list).
+// Two exclusive sums over the sequences -- pages needed and tokens -- decide everything: which entry of the
+// free list a new page takes and which packed row a token has.  A few kilobytes are read and 8 bytes per token
+// written, so the call is bound by latency: one launch, in which every CTA runs the whole scan itself (four
+// sequences per thread and pass; the lengths come from L2) and then writes only its own range of token
+// rows.  A token whose index starts a page also writes that page's table entry, so entries have one writer and
+// no CTA reads an entry that another one writes (rows on new pages take the page from the free list).
 #include <algorithm>
 #include <climits>
 
@@ -17,21 +16,25 @@
 namespace gdn {
 namespace {
 
-constexpr int kXThreads = 1024;
 constexpr int kXItems = 4;                      // sequences per thread and pass
-constexpr int kXPass = kXThreads * kXItems;
 constexpr int kXRows = 4096;                    // most token rows of a CTA
 constexpr int kXDirect = 4;                     // a thread writes so many of its sequence's rows by itself
+constexpr int kXWide = 64;                      // longer runs are for the whole CTA, shorter ones for a warp
 constexpr int kXList = kXRows / (kXDirect + 1) + 2;
 
 struct ExtendParams {
     int32_t *table;
     const int32_t *lens, *fresh, *free_pages, *free_count;
     int32_t *slot_map, *positions, *cu, *lens_out, *free_left, *status;
-    int32_t N, W, page, F, M, prefix, rows_per_cta;
+    int32_t N, W, page, shift, F, M, prefix, rows_per_cta;    // shift: page = 2^shift, or -1
 };
 
-// One sequence's rows: n < 0 marks a refused one.
+// x / page for 0 <= x < 2^32
+__device__ __forceinline__ uint32_t pages_in(const ExtendParams &P, uint32_t x) {
+    return P.shift >= 0 ? x >> P.shift : x / (uint32_t)P.page;
+}
+
+// One sequence's rows.
 struct Run {
     int64_t cu, page0;          // its first row; the pages taken before its own
     int32_t n, len, have;       // own tokens, pages it had
@@ -46,7 +49,7 @@ __device__ __forceinline__ void write_row(const ExtendParams &P, const Run &r, i
         return;
     }
     const int i = r.len + (int)(row - r.cu);
-    const int j = i / P.page, off = i - j * P.page;
+    const int j = (int)pages_in(P, i), off = i - j * P.page;
     int64_t page;
     int32_t *entry = P.table + (int64_t)r.n * P.W + j;
     if (j < r.have) {
@@ -65,8 +68,10 @@ __device__ __forceinline__ void write_row(const ExtendParams &P, const Run &r, i
     P.positions[row] = (int32_t)min((int64_t)P.prefix + i, (int64_t)INT32_MAX);
 }
 
-__global__ void __launch_bounds__(kXThreads) gdn_kv_extend_kernel(const ExtendParams P) {
-    __shared__ int64_t s_need[32], s_new[32];
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) gdn_kv_extend_kernel(const __grid_constant__ ExtendParams P) {
+    constexpr int kWarps = THREADS / 32;
+    __shared__ int64_t s_new[2][32], s_need[2][32];     // the warps' sums, of even and odd passes
     __shared__ Run s_list[kXList];
     __shared__ int s_count;
     __shared__ unsigned long long s_taken;      // pages that served sequences take
@@ -74,16 +79,17 @@ __global__ void __launch_bounds__(kXThreads) gdn_kv_extend_kernel(const ExtendPa
     const int row0 = (int)min((int64_t)blockIdx.x * P.rows_per_cta, (int64_t)P.M);
     const int row1 = (int)min((int64_t)row0 + P.rows_per_cta, (int64_t)P.M);
     const int32_t count = *P.free_count;
-    const int top = min(max(count, 0), P.F);
-    bool bad = top != count;
+    const int64_t room = (int64_t)P.W * P.page;
+    bool bad = false;
     int64_t need_before = 0, new_before = 0;    // sums of the earlier passes
-    if (tid == 0) s_taken = 0;
+    if (tid == 0) s_taken = 0, s_count = 0;
 
-    for (int base = 0, pass = 0; base < P.N; base += kXPass, ++pass) {
+    for (int64_t base = 0, pass = 0; base < P.N; base += THREADS * kXItems, ++pass) {
+        const int par = (int)(pass & 1);
         int32_t len[kXItems], w[kXItems], have[kXItems], need[kXItems];
         bool wrong[kXItems];
         int64_t my_need = 0, my_new = 0;
-        const int n0 = base + tid * kXItems;
+        const int64_t n0 = base + tid * kXItems;
 #pragma unroll
         for (int i = 0; i < kXItems; ++i) {
             const bool in = n0 + i < P.N;
@@ -92,73 +98,47 @@ __global__ void __launch_bounds__(kXThreads) gdn_kv_extend_kernel(const ExtendPa
         }
 #pragma unroll
         for (int i = 0; i < kXItems; ++i) {
-            wrong[i] = len[i] < 0 || w[i] < 0 || (int64_t)len[i] + w[i] > (int64_t)P.W * P.page;
+            wrong[i] = len[i] < 0 || w[i] < 0 || (int64_t)len[i] + w[i] > room;
             w[i] = max(w[i], 0);
             my_new += w[i];
+            // up to 2^31 - 1 + page - 1 < 2^32
+            have[i] = wrong[i] ? 0 : (int)pages_in(P, (uint32_t)len[i] + (uint32_t)(P.page - 1));
+            need[i] = wrong[i] ? 0 : (int)pages_in(P, (uint32_t)len[i] + (uint32_t)w[i] + (uint32_t)(P.page - 1)) - have[i];
+            my_need += need[i];
         }
-        // tokens first: a sequence whose rows pass M takes no pages
-        int64_t x = my_new;
+        // Both sums in one scan.  A sequence whose rows pass M is refused and takes no pages; as the rows' sum only
+        // grows, so is every sequence behind it, and counting its pages changes nothing for the others.
+        int64_t x = my_new, y = my_need;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
+            const int64_t a = __shfl_up_sync(0xffffffffu, x, o), b = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) x += a, y += b;
         }
-        __syncthreads();                        // the last pass has read s_new, s_need and the list
-        if (tid == 0) s_count = 0;
-        if (lane == 31) s_new[warp] = x;
+        if (lane == 31) s_new[par][warp] = x, s_need[par][warp] = y;
         __syncthreads();
-        if (warp == 0) {
-            int64_t t = s_new[lane];
+        int64_t cu = new_before + x - my_new, before = need_before + y - my_need;
+        {                                       // the warps before this one, and all of them
+            int64_t a = lane < kWarps ? s_new[par][lane] : 0, b = lane < kWarps ? s_need[par][lane] : 0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, t, o);
-                if (lane >= o) t += y;
+            for (int o = 1; o < kWarps; o <<= 1) {
+                const int64_t c = __shfl_up_sync(0xffffffffu, a, o), d = __shfl_up_sync(0xffffffffu, b, o);
+                if (lane >= o) a += c, b += d;
             }
-            s_new[lane] = t;
+            const int64_t pa = __shfl_sync(0xffffffffu, a, max(warp - 1, 0)), pb = __shfl_sync(0xffffffffu, b, max(warp - 1, 0));
+            if (warp > 0) cu += pa, before += pb;
+            new_before += __shfl_sync(0xffffffffu, a, kWarps - 1);
+            need_before += __shfl_sync(0xffffffffu, b, kWarps - 1);
         }
-        __syncthreads();
-        int64_t cu = new_before + x - my_new + (warp ? s_new[warp - 1] : 0);
-        new_before += s_new[31];
-        {
-            int64_t c = cu;
-#pragma unroll
-            for (int i = 0; i < kXItems; ++i) {
-                c += w[i];
-                wrong[i] = wrong[i] || c > P.M;
-                have[i] = wrong[i] ? 0 : (int)(((int64_t)len[i] + P.page - 1) / P.page);
-                need[i] = wrong[i] ? 0 : (int)(((int64_t)len[i] + w[i] + P.page - 1) / P.page) - have[i];
-                my_need += need[i];
-            }
-        }
-        x = my_need;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) s_need[warp] = x;
-        __syncthreads();
-        if (warp == 0) {
-            int64_t t = s_need[lane];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, t, o);
-                if (lane >= o) t += y;
-            }
-            s_need[lane] = t;
-        }
-        __syncthreads();
-        int64_t before = need_before + x - my_need + (warp ? s_need[warp - 1] : 0);
-        need_before += s_need[31];
-
+        const int top = min(max(count, 0), P.F);
         const bool writer = pass % gridDim.x == blockIdx.x;     // this pass's per-sequence outputs
+        bool listed = false;
 #pragma unroll
         for (int i = 0; i < kXItems; ++i) {
-            const int n = n0 + i;
+            const int64_t n = n0 + i;
             if (n < P.N) {
                 Run r;
-                r.cu = cu, r.page0 = before, r.n = n, r.len = len[i], r.have = have[i];
-                r.refused = wrong[i] || (need[i] > 0 && before + need[i] > top);
+                r.cu = cu, r.page0 = before, r.n = (int32_t)n, r.len = len[i], r.have = have[i];
+                r.refused = wrong[i] || cu + w[i] > P.M || (need[i] > 0 && before + need[i] > top);
                 r.lo = (int)min(max(cu, (int64_t)row0), (int64_t)row1);
                 r.hi = (int)min(cu + w[i], (int64_t)row1);
                 if (r.refused) bad = true;
@@ -167,37 +147,43 @@ __global__ void __launch_bounds__(kXThreads) gdn_kv_extend_kernel(const ExtendPa
                     P.cu[n] = (int32_t)min(cu, (int64_t)INT32_MAX);
                     P.lens_out[n] = r.refused ? len[i] : len[i] + w[i];
                 }
-                if (r.hi - r.lo > kXDirect) s_list[atomicAdd(&s_count, 1)] = r;
-                else
+                if (r.hi - r.lo > kXDirect) {
+                    s_list[atomicAdd(&s_count, 1)] = r;
+                    listed = true;
+                } else {
                     for (int row = r.lo; row < r.hi; ++row) write_row(P, r, row, top);
+                }
                 cu += w[i];
                 before += need[i];
             }
         }
-        __syncthreads();
-        const int listed = s_count;
-        for (int e = warp; e < listed; e += kXThreads / 32) {               // short runs: a warp each
-            const Run r = s_list[e];
-            if (r.hi - r.lo <= 256)
-                for (int row = r.lo + lane; row < r.hi; row += 32) write_row(P, r, row, top);
-        }
-        for (int e = 0; e < listed; ++e) {                                  // long ones: the CTA
-            if (s_list[e].hi - s_list[e].lo <= 256) continue;
-            const Run r = s_list[e];
-            for (int row = r.lo + tid; row < r.hi; row += kXThreads) write_row(P, r, row, top);
+        if (__syncthreads_or(listed)) {
+            const int runs = s_count;
+            for (int e = warp; e < runs; e += kWarps) {                     // short runs: a warp each
+                const Run r = s_list[e];
+                if (r.hi - r.lo <= kXWide)
+                    for (int row = r.lo + lane; row < r.hi; row += 32) write_row(P, r, row, top);
+            }
+            for (int e = 0; e < runs; ++e) {                                // long ones: the CTA
+                if (s_list[e].hi - s_list[e].lo <= kXWide) continue;
+                const Run r = s_list[e];
+                for (int row = r.lo + tid; row < r.hi; row += THREADS) write_row(P, r, row, top);
+            }
+            __syncthreads();
+            if (tid == 0) s_count = 0;          // the next pass's barrier comes before its first run
         }
     }
-    for (int64_t row = max(new_before, (int64_t)row0) + tid; row < row1; row += kXThreads) {     // padding rows
+    for (int64_t row = max(new_before, (int64_t)row0) + tid; row < row1; row += THREADS) {     // padding rows
         P.slot_map[row] = -1;
         P.positions[row] = -1;
     }
-    __syncthreads();
     if (blockIdx.x == 0) {
-        if (tid == 0) {
+        const int top = min(max(count, 0), P.F);
+        if (tid == 0) {                         // the last pass's barrier came after every atomicMax
             P.cu[P.N] = (int32_t)min(new_before, (int64_t)INT32_MAX);
             *P.free_left = top - (int)s_taken;
         }
-        if (bad && P.status) atomicExch(P.status, (int32_t)GDN_ERR_INVALID_ARG);
+        if ((bad || top != count) && P.status) atomicExch(P.status, (int32_t)GDN_ERR_INVALID_ARG);
     }
 }
 
@@ -217,7 +203,7 @@ extern "C" gdn_status gdn_kv_extend(const gdn_kv_extend_desc *D, int32_t *block_
                                     int32_t *slot_map, int32_t *positions, int32_t *cu_new, int32_t *seq_lens_out,
                                     int32_t *free_left, int32_t *device_status, gdn_stream_t stream) {
     if (!D || D->num_seqs < 1 || D->table_width < 1 || D->page_size < 1 || D->num_free < 0 || D->max_new_tokens < 0 ||
-        D->prefix_len < 0 || D->reserved[0] || D->reserved[1] || D->num_seqs > INT32_MAX - 2 * kXPass)
+        D->prefix_len < 0 || D->reserved[0] || D->reserved[1] || D->num_seqs > INT32_MAX - 8192)
         return GDN_ERR_INVALID_ARG;
     if (!block_table || !seq_lens || !new_lens || !free_count || !cu_new || !seq_lens_out || !free_left ||
         (D->num_free > 0 && !free_pages) || (D->max_new_tokens > 0 && (!slot_map || !positions)))
@@ -238,12 +224,18 @@ extern "C" gdn_status gdn_kv_extend(const gdn_kv_extend_desc *D, int32_t *block_
     }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (device_status && cudaMemsetAsync(device_status, 0, sizeof(int32_t), st) != cudaSuccess) return GDN_ERR_CUDA;
-    ExtendParams P = {block_table, seq_lens, new_lens, free_pages, free_count, slot_map, positions, cu_new, seq_lens_out,
-                      free_left, device_status, D->num_seqs, D->table_width, D->page_size, D->num_free,
-                      D->max_new_tokens, D->prefix_len, 0};
-    // token rows per CTA: a CTA's threads' worth, more only when that would pass one CTA per SM
-    P.rows_per_cta = (int)std::min<int64_t>(kXRows, std::max<int64_t>(kXThreads, (M + 147) / 148));
-    const unsigned grid = (unsigned)std::max<int64_t>(1, (M + P.rows_per_cta - 1) / P.rows_per_cta);
-    gdn_kv_extend_kernel<<<grid, kXThreads, 0, st>>>(P);
+    int shift = -1;
+    if ((D->page_size & (D->page_size - 1)) == 0)
+        for (shift = 0; (1 << shift) < D->page_size;) ++shift;
+    // Small CTAs while one pass of them covers the sequences (their barriers are cheaper), large ones for fewer
+    // passes after that; a row per thread, more only when that would pass two CTAs per SM.
+    const int threads = N <= 256 * kXItems ? 256 : 1024;
+    const int32_t rows = (int32_t)std::min<int64_t>(kXRows, std::max<int64_t>(threads, (M + 295) / 296));
+    const ExtendParams P = {block_table, seq_lens, new_lens, free_pages, free_count, slot_map, positions, cu_new,
+                            seq_lens_out, free_left, device_status, D->num_seqs, D->table_width, D->page_size, shift,
+                            D->num_free, D->max_new_tokens, D->prefix_len, rows};
+    const unsigned grid = (unsigned)std::max<int64_t>(1, (M + rows - 1) / rows);
+    if (threads == 256) gdn_kv_extend_kernel<256><<<grid, 256, 0, st>>>(P);
+    else gdn_kv_extend_kernel<1024><<<grid, 1024, 0, st>>>(P);
     return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
