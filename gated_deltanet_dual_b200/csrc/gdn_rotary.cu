@@ -9,7 +9,8 @@
 // Bound by memory: every element is read and written once.  A CTA takes a few rows; its threads
 // first compute the rows' (cos, sin) once for all heads into shared memory, then each thread keeps
 // one column unit (two 16-byte vectors whose elements pair up, or one vector of interleaved
-// pairs) and walks over (row, head), holding its unit's cos and sin in registers within a row.
+// pairs) and walks over (row, head), a few heads at a time, holding its unit's cos and sin in registers
+// within a row.
 #include <algorithm>
 #include <cmath>
 
@@ -35,39 +36,42 @@ struct RotaryParams {
     float scale, sign;
 };
 
-// Sixteen bytes as packed elements.
-template <typename T> struct Vec;
-template <> struct Vec<float> {
-    static constexpr int N = 4;
-    static __device__ __forceinline__ void load(const float *p, float (&x)[4]) {
-        const float4 u = *reinterpret_cast<const float4 *>(p);
-        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+// The bits of a unit: 16 bytes, or one element; its values as floats, and back with one rounding.
+template <int BYTES> struct RawOf;
+template <> struct RawOf<16> { using type = uint4; };
+template <> struct RawOf<4> { using type = uint32_t; };
+template <> struct RawOf<2> { using type = uint16_t; };
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
+template <typename T> struct Codec;
+template <> struct Codec<float> {
+    static __device__ __forceinline__ void get(uint4 u, float (&x)[4]) {
+        x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
     }
-    static __device__ __forceinline__ void store(float *p, const float (&x)[4]) {
-        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    static __device__ __forceinline__ uint4 put(const float (&x)[4]) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
     }
+    static __device__ __forceinline__ void get(uint32_t u, float (&x)[1]) { x[0] = __uint_as_float(u); }
+    static __device__ __forceinline__ uint32_t put(const float (&x)[1]) { return __float_as_uint(x[0]); }
 };
-template <> struct Vec<__nv_bfloat16> {
-    static constexpr int N = 8;
-    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&x)[8]) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+template <> struct Codec<__nv_bfloat16> {
+    static __device__ __forceinline__ void get(uint4 u, float (&x)[8]) {
+        x[0] = bf16_lo(u.x), x[1] = bf16_hi(u.x), x[2] = bf16_lo(u.y), x[3] = bf16_hi(u.y);
+        x[4] = bf16_lo(u.z), x[5] = bf16_hi(u.z), x[6] = bf16_lo(u.w), x[7] = bf16_hi(u.w);
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&x)[8]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&b);
-        }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    static __device__ __forceinline__ uint4 put(const float (&x)[8]) {
+        return make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
     }
+    static __device__ __forceinline__ void get(uint16_t u, float (&x)[1]) { x[0] = bf16_lo(u); }
+    static __device__ __forceinline__ uint16_t put(const float (&x)[1]) { return (uint16_t)bf16_pair(x[0], 0.f); }
 };
+template <typename T, typename R, int N> __device__ __forceinline__ void unpack(R u, float (&x)[N]) { Codec<T>::get(u, x); }
+template <typename T, int N> __device__ __forceinline__ auto pack(const float (&x)[N]) { return Codec<T>::put(x); }
 
 // (cos, sin) of one (position, pair), scaled; sin signed.
 __device__ __forceinline__ float2 unit_of(int32_t position, uint64_t turn, float scale, float sign) {
@@ -111,7 +115,7 @@ template <typename T, bool IL, bool APPEND, bool VEC>
 __global__ void __launch_bounds__(kRThreads) gdn_rotary_kernel(const __grid_constant__ RotaryParams P) {
     __shared__ float2 cs[kRMaxRows * (kRMaxRot / 2)];
     __shared__ int64_t s_slot[kRMaxRows];
-    constexpr int VN = VEC ? Vec<T>::N : 1;
+    constexpr int VN = VEC ? 16 / (int)sizeof(T) : 1;
     constexpr int PU = !VEC ? 1 : IL ? VN / 2 : VN;         // pairs of a rotated unit
     const int tid = threadIdx.x, np = P.rot >> 1;
     const int64_t row0 = (int64_t)blockIdx.x * P.rows_per_cta;
@@ -148,68 +152,72 @@ __global__ void __launch_bounds__(kRThreads) gdn_rotary_kernel(const __grid_cons
     const int e1 = (IL && !VEC) ? e0 + 1 : e0 + np;         // its partner's (half layout, or scalar pairs)
     float2 w[PU];
     int wrow = -1;
+    // kBatch heads at a time: all their loads are on their way before the first store
+    constexpr int kBatch = VEC ? (IL ? 4 : 2) : 1;
+    constexpr int kBytes = VEC ? 16 : sizeof(T);
+    using Raw = typename RawOf<kBytes>::type;
     while (row < nrows) {
-        const int64_t slot = APPEND ? s_slot[row] : 0;
-        if (!APPEND || slot >= 0) {
-            const HeadRef<T, APPEND> h(P, row0 + row, head, slot);
-            if (wrow != row && !plain) {
-                wrow = row;
+        Raw a[kBatch], b[kBatch];
+        T *dst[kBatch];
+        int rows[kBatch];
+        bool turn[kBatch];
+        const bool second = !plain && !(IL && VEC);        // the unit's partner lies elsewhere
 #pragma unroll
-                for (int i = 0; i < PU; ++i) w[i] = cs[row * np + u * PU + i];
-            }
-            if constexpr (VEC) {
-                if (plain) {
-                    *reinterpret_cast<uint4 *>(h.dst + e0) = *reinterpret_cast<const uint4 *>(h.src + e0);
-                } else if (!h.turn) {
-                    const uint4 a = *reinterpret_cast<const uint4 *>(h.src + e0);
-                    if (!IL) {
-                        const uint4 b = *reinterpret_cast<const uint4 *>(h.src + e1);
-                        *reinterpret_cast<uint4 *>(h.dst + e1) = b;
-                    }
-                    *reinterpret_cast<uint4 *>(h.dst + e0) = a;
-                } else if constexpr (IL) {
-                    float x[VN];
-                    Vec<T>::load(h.src + e0, x);
-#pragma unroll
-                    for (int i = 0; i < PU; ++i) {
-                        const float a = x[2 * i], b = x[2 * i + 1];
-                        x[2 * i] = a * w[i].x - b * w[i].y;
-                        x[2 * i + 1] = a * w[i].y + b * w[i].x;
-                    }
-                    Vec<T>::store(h.dst + e0, x);
-                } else {
-                    float x[VN], y[VN];
-                    Vec<T>::load(h.src + e0, x);
-                    Vec<T>::load(h.src + e1, y);
-#pragma unroll
-                    for (int i = 0; i < VN; ++i) {
-                        const float a = x[i], b = y[i];
-                        x[i] = a * w[i].x - b * w[i].y;
-                        y[i] = a * w[i].y + b * w[i].x;
-                    }
-                    Vec<T>::store(h.dst + e0, x);
-                    Vec<T>::store(h.dst + e1, y);
+        for (int i = 0; i < kBatch; ++i) {
+            dst[i] = nullptr;
+            rows[i] = row;
+            turn[i] = false;
+            if (row < nrows) {
+                const int64_t slot = APPEND ? s_slot[row] : 0;
+                if (!APPEND || slot >= 0) {
+                    const HeadRef<T, APPEND> h(P, row0 + row, head, slot);
+                    dst[i] = h.dst;
+                    turn[i] = h.turn && !plain;
+                    a[i] = *reinterpret_cast<const Raw *>(h.src + e0);
+                    if (second) b[i] = *reinterpret_cast<const Raw *>(h.src + e1);
                 }
-            } else {
-                if (plain) {
-                    h.dst[e0] = h.src[e0];
-                } else {
-                    const T ta = h.src[e0], tb = h.src[e1];
-                    if (!h.turn) {
-                        h.dst[e0] = ta;
-                        h.dst[e1] = tb;
-                    } else {
-                        const float a = to_f32(ta), b = to_f32(tb);
-                        h.dst[e0] = from_f32<T>(a * w[0].x - b * w[0].y);
-                        h.dst[e1] = from_f32<T>(a * w[0].y + b * w[0].x);
-                    }
+                head += groups;
+                while (head >= heads) {
+                    head -= heads;
+                    ++row;
                 }
             }
         }
-        head += groups;
-        while (head >= heads) {
-            head -= heads;
-            ++row;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (!dst[i]) continue;
+            if (turn[i]) {
+                if (wrow != rows[i]) {
+                    wrow = rows[i];
+#pragma unroll
+                    for (int j = 0; j < PU; ++j) w[j] = cs[wrow * np + u * PU + j];
+                }
+                if constexpr (IL && VEC) {
+                    float x[VN];
+                    unpack<T>(a[i], x);
+#pragma unroll
+                    for (int j = 0; j < PU; ++j) {
+                        const float p = x[2 * j], q = x[2 * j + 1];
+                        x[2 * j] = p * w[j].x - q * w[j].y;
+                        x[2 * j + 1] = p * w[j].y + q * w[j].x;
+                    }
+                    a[i] = pack<T>(x);
+                } else {
+                    float x[VN], y[VN];
+                    unpack<T>(a[i], x);
+                    unpack<T>(b[i], y);
+#pragma unroll
+                    for (int j = 0; j < VN; ++j) {
+                        const float p = x[j], q = y[j];
+                        x[j] = p * w[j].x - q * w[j].y;
+                        y[j] = p * w[j].y + q * w[j].x;
+                    }
+                    a[i] = pack<T>(x);
+                    b[i] = pack<T>(y);
+                }
+            }
+            *reinterpret_cast<Raw *>(dst[i] + e0) = a[i];
+            if (second) *reinterpret_cast<Raw *>(dst[i] + e1) = b[i];
         }
     }
 }
