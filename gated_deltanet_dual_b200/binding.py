@@ -646,8 +646,9 @@ def backward_conv_workspace_size(desc: Desc, doc_offsets) -> int:
 
 
 # ----------------------------------------------------------------------------- serving calls
-# The calls below are made once per layer and decode step, so their checks are kept short: one comparison
-# per property, and the full message only on the way to an exception.
+# The calls below are made once per layer and decode step, where a few microseconds on the host count: all
+# properties are tested in one expression, and only a call that fails it goes through the checks that
+# name what is wrong.
 def _want(t: torch.Tensor, name: str, shape, dtype, index: int):
     """t is a contiguous CUDA tensor of this shape and dtype on device `index`, or raises."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
@@ -680,20 +681,15 @@ def _cuda_index(t: torch.Tensor) -> int:
     return index
 
 
-def _raw_stream(index: int, stream) -> int:
-    """The given stream, or the current one of device `index`."""
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream
-
-
 def _call(name: str, index: int, stream, fresh, *args):
     """Calls the library on device `index` and raises on an error.  Tensors that the caller allocated itself
     (fresh) are kept alive for a stream that is not the current one."""
-    fn = getattr(load_library(), name)
-    if torch.cuda.current_device() == index:
-        st = fn(*args, _raw_stream(index, stream))
+    fn = getattr(_lib or load_library(), name)
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
     else:
         with torch.cuda.device(index):
-            st = fn(*args, _raw_stream(index, stream))
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
     if stream is not None:
         other = torch.cuda.ExternalStream(stream, device=index)
         for t in fresh:
@@ -822,12 +818,15 @@ def kv_extend(block_table, seq_lens, new_lens, free_pages, free_count, page_size
         raise ValueError("block_table must be [N, W]")
     N, W = block_table.shape
     F, M = free_pages.numel(), tables._sizes[1]
-    _want(block_table, "block_table", (N, W), i32, index)
-    _want(seq_lens, "seq_lens", (N,), i32, index)
-    _want(new_lens, "new_lens", (N,), i32, index)
-    _want(free_pages, "free_pages", (F,), i32, index)
-    _want(free_count, "free_count", (1,), i32, index)
-    if tables._sizes[0] != N or tables._index != index:
+    if not (tables._sizes[0] == N and tables._index == index and seq_lens.shape == new_lens.shape == (N,)
+            and free_pages.shape == (F,) and free_count.shape == (1,) and block_table.dtype is i32
+            and seq_lens.dtype is i32 and new_lens.dtype is i32 and free_pages.dtype is i32 and free_count.dtype is i32
+            and seq_lens.get_device() == new_lens.get_device() == free_pages.get_device() == free_count.get_device() == index
+            and block_table.is_contiguous() and seq_lens.is_contiguous() and new_lens.is_contiguous()
+            and free_pages.is_contiguous()):
+        for t, name, shape in ((block_table, "block_table", (N, W)), (seq_lens, "seq_lens", (N,)), (new_lens, "new_lens", (N,)),
+                               (free_pages, "free_pages", (F,)), (free_count, "free_count", (1,))):
+            _want(t, name, shape, i32, index)
         raise ValueError(f"tables are made for {tables._sizes[0]} sequences on {tables.free_left.device}, not for {N} on cuda:{index}")
     if device_status is not None:
         _want(device_status, "device_status", (1,), i32, index)
@@ -844,23 +843,33 @@ def rotary_append(q, k, v, positions, slot_map, table: RotaryTable, k_cache, v_c
     q_out, k [R, H_kv, d] rotated into k_cache [P, p, H_kv, d] and v copied into v_cache, at slot_map [R]
     int32.  Rows with slot -1 are padding and are left as they were.  Returns q_out."""
     index, io = _cuda_index(q), q.dtype
-    if q.ndim != 3 or k.ndim != 3 or k_cache.ndim != 4:
-        raise ValueError("q, k and v must be [R, heads, d] and the caches [P, p, H_kv, d]")
+    if q.ndim != 3 or k.ndim != 3 or v.ndim != 3 or k_cache.ndim != 4 or (q_out is not None and q_out.ndim != 3):
+        raise ValueError("q, k, v and q_out must be [R, heads, d] and the caches [P, p, H_kv, d]")
     R, H, d = q.shape
     Hkv, (P, page) = k.shape[1], k_cache.shape[:2]
     fresh = ()
     if q_out is None:
         q_out = torch.empty(R, H, d, dtype=io, device=q.device)
         fresh = (q_out,)
-    strides = (_rows(q, "q", (R, H, d), io, index) + _rows(k, "k", (R, Hkv, d), io, index)
-               + _rows(v, "v", (R, Hkv, d), io, index) + _rows(q_out, "q_out", (R, H, d), io, index))
-    _want(k_cache, "k_cache", (P, page, Hkv, d), io, index)
-    _want(v_cache, "v_cache", (P, page, Hkv, d), io, index)
-    _want(positions, "positions", (R,), torch.int32, index)
-    _want(slot_map, "slot_map", (R,), torch.int32, index)
+    (qr, qh, q1), (kr, kh, k1), (vr, vh, v1), (outr, outh, out1) = q.stride(), k.stride(), v.stride(), q_out.stride()
+    if not (q1 == k1 == v1 == out1 == 1 and k.shape[0] == R and k.shape[2] == d and v.shape == k.shape
+            and q_out.shape == q.shape and k_cache.shape == v_cache.shape == (P, page, Hkv, d) and k.dtype is io
+            and v.dtype is io and q_out.dtype is io and k_cache.dtype is io and v_cache.dtype is io
+            and positions.dtype is torch.int32 and slot_map.dtype is torch.int32
+            and positions.shape == slot_map.shape == (R,) and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and positions.is_contiguous() and slot_map.is_contiguous()
+            and k.get_device() == v.get_device() == q_out.get_device() == k_cache.get_device() == v_cache.get_device()
+            == positions.get_device() == slot_map.get_device() == index):
+        for t, name, heads in ((q, "q", H), (k, "k", Hkv), (v, "v", Hkv), (q_out, "q_out", H)):
+            _rows(t, name, (R, heads, d), io, index)
+        _want(k_cache, "k_cache", (P, page, Hkv, d), io, index)
+        _want(v_cache, "v_cache", (P, page, Hkv, d), io, index)
+        _want(positions, "positions", (R,), torch.int32, index)
+        _want(slot_map, "slot_map", (R,), torch.int32, index)
     if device_status is not None:
         _want(device_status, "device_status", (1,), torch.int32, index)
-    desc = AppendDesc(R, H, Hkv, d, table._args[0], table._args[1], page, P, _dtype_code(q), table._args[2], *strides)
+    desc = AppendDesc(R, H, Hkv, d, table._args[0], table._args[1], page, P, _dtype_code(q), table._args[2],
+                      qr, qh, kr, kh, vr, vh, outr, outh)
     _call("gdn_rotary_append", index, stream, fresh, ctypes.byref(desc), table._on(index), positions.data_ptr(),
           slot_map.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), None if device_status is None else device_status.data_ptr())
@@ -890,12 +899,17 @@ def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len, block_table,
     N, L, H, d = shape = q.shape
     P, page, Hkv = k_cache.shape[:3]
     W = block_table.shape[1]
-    cache = (P, page, Hkv, d)
-    _want(q, "q", shape, io, index)
-    _want(k_cache, "k_cache", cache, io, index)
-    _want(v_cache, "v_cache", cache, io, index)
-    _want(block_table, "block_table", (N, W), torch.int32, index)
-    _want(seq_lens, "seq_lens", (N,), torch.int32, index)
+    i32 = torch.int32
+    if not (k_cache.dtype is io and v_cache.dtype is io and block_table.dtype is i32 and seq_lens.dtype is i32
+            and k_cache.shape[3] == d and v_cache.shape == k_cache.shape and block_table.shape[0] == N
+            and seq_lens.shape == (N,) and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and block_table.is_contiguous() and seq_lens.is_contiguous()
+            and k_cache.get_device() == v_cache.get_device() == block_table.get_device() == seq_lens.get_device() == index):
+        _want(q, "q", shape, io, index)
+        _want(k_cache, "k_cache", (P, page, Hkv, d), io, index)
+        _want(v_cache, "v_cache", (P, page, Hkv, d), io, index)
+        _want(block_table, "block_table", (N, W), i32, index)
+        _want(seq_lens, "seq_lens", (N,), i32, index)
     if scale is not None and not scale > 0:
         raise ValueError("scale must be positive")
     if prefix_len:
