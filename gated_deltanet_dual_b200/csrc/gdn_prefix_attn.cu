@@ -627,13 +627,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // requests of up to 1024 tokens: 35 against 40 us); elsewhere registers allow two CTAs, or tiles are
 // small.
 template <int D, int NT>
-constexpr int warp_stages() { return D == 128 && NT == 1 ? 2 : 3; }
+constexpr int warp_stages() { return D == 128 ? 2 : 3; }
 template <int D, int NT>
 constexpr int warp_smem() { return warp_stages<D, NT>() * 2 * kWKeys * D * 2 + 1024; }
 
 // NT: column tiles of 8 rows.
 template <int D, int NT>
-__global__ void __maxnreg__(NT == 1 ? 112 : 168)
+__global__ void __maxnreg__(112)
 gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ PrefixMaps M) {
     constexpr int kHalves = D / 64;
     constexpr int kHalfBytes = kWKeys * 128;
