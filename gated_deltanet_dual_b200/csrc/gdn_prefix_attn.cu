@@ -1066,14 +1066,21 @@ struct Plan {
     size_t off_status, off_ml, off_o, bytes;
 };
 
-// Splits of `tiles` key tiles over `base` equal work items: waves of CTAs times a CTA's tiles, three more
-// for its set-up and its part of the combine step.
-int best_split(int64_t base, int64_t tiles) {
+// Splits of `tiles` key tiles over `base` equal lists for gdn_tile_attn_kernel, beside other work of `beside`
+// SM-microseconds in the same call.  A CTA takes tile_us a key tile and kStartUs for its start and end (measured at
+// two row tiles, d = 128: 2.25, or 2.7 beside other CTAs' loads, and 12.7); the call takes as long as its waves of CTAs, or as all its work on all
+// SMs, and each part a little in the combine step.  With own keys beside it a prefix is thus cut into fewer
+// parts than would fill the GPU (8192 keys for 64 requests of up to 1024 own tokens: 8 parts, 48 us; 16
+// parts, 58 us).
+int tile_split(int64_t base, int64_t tiles, double beside) {
+    constexpr double kStartUs = 12.7, kPartUs = 0.3;
+    const double tile_us = beside > 0.0 ? 2.7 : 2.25;
     int best = 1;
     double cost = 1e300;
     for (int s = 1; s <= kMaxSplits && s <= tiles; ++s) {
-        const double waves = (double)((base * s + kSms - 1) / kSms);
-        const double c = waves * ((double)((tiles + s - 1) / s) + 3.0);
+        const double cta = (double)((tiles + s - 1) / s) * tile_us + kStartUs;
+        const double waves = (double)((base * s + kSms - 1) / kSms) * cta;
+        const double c = std::max(waves, ((double)(base * s) * cta + beside) / kSms) + kPartUs * s;
         if (c < cost * 0.999) cost = c, best = s;
     }
     return best;
@@ -1099,9 +1106,11 @@ Plan plan_of(const gdn_prefix_attn_desc *D) {
     p.own_tiles = p.own_warp ? 1 : (int)((per_seq + kRows - 1) / kRows);
     const int64_t prefix_base = (int64_t)D->num_kv_heads * p.prefix_tiles;
     const int64_t own_base = (int64_t)D->num_seqs * D->num_kv_heads * p.own_tiles;
+    // own keys beside the prefix, at half of the tables' room and 6.4 TB/s
+    const double own_us = (double)D->num_seqs * own_room * D->num_kv_heads * D->head_dim * 4 / 2 / 6.4e6 * kSms;
     p.prefix_splits = !D->prefix_len ? 0 : p.prefix_warp ? warp_split(prefix_base, D->prefix_len)
-                                                         : best_split(prefix_base, ((int64_t)D->prefix_len + kTile - 1) / kTile);
-    p.own_splits = !own_room ? 0 : p.own_warp ? warp_split(own_base, own_room) : best_split(own_base, (own_room + kTile - 1) / kTile);
+                                                         : tile_split(prefix_base, ((int64_t)D->prefix_len + kTile - 1) / kTile, own_us);
+    p.own_splits = !own_room ? 0 : p.own_warp ? warp_split(own_base, own_room) : tile_split(own_base, (own_room + kTile - 1) / kTile, 0.0);
     p.prefix_items = (int64_t)D->num_kv_heads * p.prefix_tiles * p.prefix_splits;
     p.own_items = (int64_t)D->num_seqs * D->num_kv_heads * p.own_tiles * p.own_splits;
     p.parts = p.prefix_splits + p.own_splits;
