@@ -12,12 +12,12 @@
 //
 // gdn_tile_attn_kernel -- one CTA = up to 256 query rows (row tiles A and B of 128) x a range of 128-key
 // tiles of one key/value head.  Warp 8 loads K and V tiles page by page by TMA into a ring, warp 9 issues the
-// MMAs, warp 10 cleans V rows that must not be seen; warps 0-3 and 4-7 are the softmax of A and B (thread = row =
+// MMAs and cleans V rows that must not be seen; warps 0-3 and 4-7 are the softmax of A and B (thread = row =
 // TMEM lane).  The tensor pipe runs S = Q K^T and O += P V of one row tile while the other's softmax runs: S_A,
-// S_B, then per key tile P_A V, S_A(next), P_B V, S_B(next).  P (bf16) overwrites S from its first columns on; MMAs
-// of one issuing thread run in order, so S(next) follows the product that reads P, and a thread that sees S(next)
-// also knows that product done and may rescale O.  160 KB of shared memory and 43,008 registers leave room on the
-// SM for a CTA of the other kernel, whose loads fill the time in which this one computes.
+// S_B, then per key tile P_A V, S_A(next), P_B V, S_B(next).  P (bf16) overwrites S from its first columns on;
+// S(next) waits for the product that reads P, so a thread that sees S(next) may also rescale O.  160 KB of shared
+// memory and 80 registers a thread leave room on the SM for a CTA of the other kernel, whose loads fill
+// the time in which this one computes.
 //
 // gdn_warp_attn_kernel -- few query rows of a key list (L (H / H_kv) <= 16: a decode step): bound by
 // reading K and V, and a 128-row tile would be padding.  One CTA = (key list, key/value head, split),
@@ -53,7 +53,7 @@ using namespace sm100;
 constexpr int kTile = 128;                     // keys of a tile, rows of a row tile
 constexpr int kRows = 2 * kTile;               // rows of a CTA
 constexpr int kStages = 3;                     // K and V tiles in flight (four and five changed nothing)
-constexpr int kTThreads = 384;                 // eight softmax warps; loads, S, cleaning, P V
+constexpr int kTThreads = 320;                 // eight softmax warps, loads, MMAs
 constexpr int kTRegs = 80;                     // with 160 KB of shared memory: leaves room for a CTA of few rows
 constexpr int kWKeys = 64;                     // gdn_warp_attn_kernel: keys of a tile (16 per warp)
 constexpr int kWThreads = 160;                 // four warps of arithmetic and one that loads
@@ -242,7 +242,7 @@ struct PrefixMaps {
 // Barriers and words of a tile CTA, behind its tiles in the dynamic shared memory.
 struct TileCtrl {
     uint64_t full[kStages], empty[kStages];
-    uint64_t bar_s[2], bar_p[2], bar_o[2], bar_clean, bar_drain;   // S complete, P written, O complete, V cleaned
+    uint64_t bar_s[2], bar_p[2], bar_v[2], bar_o[2], bar_drain;    // S complete, P written, P V done, O complete
     uint32_t tmem;
     int abort, status;
 };
@@ -256,8 +256,8 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
     extern __shared__ uint8_t smraw[];         // no static part: it starts on a 1024-byte boundary (checked below)
     uint8_t *sm_q = smraw, *sm_kv = sm_q + 2 * kTileBytes;
     TileCtrl &ctrl = *reinterpret_cast<TileCtrl *>(sm_kv + kStages * kTileBytes);
-    uint64_t *full = ctrl.full, *empty = ctrl.empty, *bar_s = ctrl.bar_s, *bar_p = ctrl.bar_p, *bar_o = ctrl.bar_o;
-    uint64_t &bar_clean = ctrl.bar_clean, &bar_drain = ctrl.bar_drain;
+    uint64_t *full = ctrl.full, *empty = ctrl.empty, *bar_s = ctrl.bar_s, *bar_p = ctrl.bar_p, *bar_v = ctrl.bar_v, *bar_o = ctrl.bar_o;
+    uint64_t &bar_drain = ctrl.bar_drain;
     uint32_t &s_tmem = ctrl.tmem;
     int &s_abort = ctrl.abort, &s_status = ctrl.status;
 
@@ -314,9 +314,9 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&bar_s[i], 1);
                 mbar_init(&bar_p[i], 4);
+                mbar_init(&bar_v[i], 1);
                 mbar_init(&bar_o[i], 1);
             }
-            mbar_init(&bar_clean, 1);
             mbar_init(&bar_drain, 1);
             fence_mbar_init();
             fence_async_smem();
@@ -365,7 +365,7 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
         }
         if (atomicExch(&s_abort, 1) == 0) atomicExch(&s_status, (int)GDN_ERR_TIMEOUT | where << 16);
     };
-    // V rows from key `newest` on are not for every query row (see the file comment): warp 10 cleans their tiles
+    // keys from this one on are not for every query row
     const int newest = (w.n >= 0 && P.causal) ? w.keys - (P.L - 1) : w.keys;
 
     if (warp == 8) {
@@ -398,7 +398,36 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
             mma_commit(&bar_s[t]);
             if (t == two) mma_commit(&empty[slot]);
         };
-        int slot = 0, cleaned = 0;
+        // V rows of the list from key `newest` on are not for every query row (see the file comment)
+        auto clean = [&](int slot, int key0) {
+                uint8_t *v = sm_kv + slot * kTileBytes;
+                const int last = min(kTile, w.keys - key0);          // rows [last, 128) are behind the list's end
+                for (int i = lane; i < (kTile - last) * (D / 8); i += 32) {
+                    const int r = last + i / (D / 8), c = i % (D / 8);
+                    *reinterpret_cast<uint4 *>(v + (c >> 3) * (kTile * 128) + sw128_off(r, c & 7)) = make_uint4(0, 0, 0, 0);
+                }
+                const int lo = max(newest - key0, 0);                // rows [lo, last) are visible to some rows only
+                bool found = false;
+                for (int i = lane; i < (last - lo) * (D / 8); i += 32) {
+                    const int r = lo + i / (D / 8), c = i % (D / 8);
+                    uint32_t *p = reinterpret_cast<uint32_t *>(v + (c >> 3) * (kTile * 128) + sw128_off(r, c & 7));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t x = p[e];
+                        const bool a = (x & 0x7f80u) == 0x7f80u, b = (x & 0x7f800000u) == 0x7f800000u;
+                        if (a) x &= 0xffff0000u;
+                        if (b) x &= 0xffffu;
+                        if (a || b) {
+                            p[e] = x;
+                            found = true;
+                        }
+                    }
+                }
+                if (found) atomicOr(&s_status, kItemNonfinite);
+                fence_async_smem();
+                __syncwarp();
+        };
+        int slot = 0;
         uint32_t phase = 0;
         auto take = [&](int where) {           // the next tile of the ring
             const int s = slot;
@@ -417,7 +446,7 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
         for (int j = 0; j < tiles; ++j, end += kTile) {
             const bool next = j + 1 < tiles;
             const int v = take(3);
-            if (end > newest) wait(&bar_clean, cleaned++ & 1, 4);
+            if (end > newest) clean(v, end - kTile);               // while the softmax is at work
             if (next) k = take(5);
             for (int t = 0; t <= two; ++t) {
                 wait(&bar_p[t], j & 1, 6);
@@ -426,11 +455,18 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)               // O_t (+)= P_t V
                         mma_bf16_ts(tb + T_O + 128 * t, tb + T_S + 128 * t + kk * 8, dv + v * kStep + kk * 128, idesc_o, j > 0 || kk > 0);
+                    mma_commit(&bar_v[t]);
                     if (t == two) mma_commit(&empty[v]);
-                    if (next) score(t, k);
-                    else mma_commit(&bar_o[t]);
+                    if (!next) mma_commit(&bar_o[t]);
                 }
                 __syncwarp();
+                // S(next) is written over P: products with different accumulators are not ordered by themselves
+                wait(&bar_v[t], j & 1, 5);
+                if (next) {
+                    tc_fence_after();
+                    if (elect_one()) score(t, k);
+                    __syncwarp();
+                }
             }
             if (__any_sync(0xffffffffu, stopped())) break;
         }
@@ -439,43 +475,7 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
             mbar_wait(&bar_drain, 0, kDrainWaitIters);
         }
         __syncwarp();
-    } else if (warp == 10) {
-        // ---------------------------------------------------------------- V rows not to be seen
-        for (int j = 0; j < tiles; ++j) {
-            if ((w.t0 + j + 1) * kTile <= newest) continue;
-            const int iv = 2 * j + 1, sv = iv % kStages, key0 = (w.t0 + j) * kTile;
-            wait(&full[sv], (iv / kStages) & 1, 9);
-            __syncwarp();
-            if (__any_sync(0xffffffffu, stopped())) break;
-            uint8_t *v = sm_kv + sv * kTileBytes;
-            const int last = min(kTile, w.keys - key0);          // rows [last, 128) are behind the list's end
-            for (int i = lane; i < (kTile - last) * (D / 8); i += 32) {
-                const int r = last + i / (D / 8), c = i % (D / 8);
-                *reinterpret_cast<uint4 *>(v + (c >> 3) * (kTile * 128) + sw128_off(r, c & 7)) = make_uint4(0, 0, 0, 0);
-            }
-            const int lo = max(newest - key0, 0);                // rows [lo, last) are visible to some rows only
-            bool found = false;
-            for (int i = lane; i < (last - lo) * (D / 8); i += 32) {
-                const int r = lo + i / (D / 8), c = i % (D / 8);
-                uint32_t *p = reinterpret_cast<uint32_t *>(v + (c >> 3) * (kTile * 128) + sw128_off(r, c & 7));
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t x = p[e];
-                    const bool a = (x & 0x7f80u) == 0x7f80u, b = (x & 0x7f800000u) == 0x7f800000u;
-                    if (a) x &= 0xffff0000u;
-                    if (b) x &= 0xffffu;
-                    if (a || b) {
-                        p[e] = x;
-                        found = true;
-                    }
-                }
-            }
-            if (found) atomicOr(&s_status, kItemNonfinite);
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_clean);
-        }
-    } else if (warp < 8) {
+    } else {
         // ---------------------------------------------------------------- softmax
         const int t = warp >> 2, quad = warp & 3, r = tid;                     // row of the CTA = thread
         const bool live = r < w.nrows, warp_live = (warp << 5) < w.nrows;

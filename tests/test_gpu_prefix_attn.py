@@ -317,3 +317,19 @@ def test_another_device_than_the_current_one():
     want = _run(p, True)
     other = {k: v.to("cuda:1") if torch.is_tensor(v) else v for k, v in p.items()}
     assert torch.equal(b.prefix_attention(**other).to("cuda:0"), want)
+
+
+@pytest.mark.parametrize("N,L,H,Hkv,d,page,prefix,own", [(32, 4, 32, 8, 128, 64, 2500, False), (24, 8, 16, 16, 64, 32, 1001, True),
+                                                           (64, 1, 32, 8, 128, 16, 3000, True), (300, 1, 4, 2, 64, 16, 129, True)])
+def test_every_call_gives_the_same_bits(N, L, H, Hkv, d, page, prefix, own):
+    """Many calls back to back: lists that end inside a key tile, several rounds of every ring, both kernels at
+    once.  (A value tile cleaned before it had landed showed here once in some thousand calls.)"""
+    lens = np.random.default_rng(N).integers(8, 900, N).tolist() if own else [0] * N
+    p = _problem(N, L, H, Hkv, d, page, prefix, lens, W=None if own else 0, seed=15)
+    ws = b.Workspace(1 << 27)
+    outs = [b.prefix_attention(**p, workspace=ws) for _ in range(5)]
+    base = max(outs, key=lambda x: sum(torch.equal(x, y) for y in outs))
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(4000):
+        wrong += (b.prefix_attention(**p, workspace=ws) != base).any()
+    assert int(wrong) == 0 and b.read_device_status(ws) == b.GDN_OK
