@@ -11,13 +11,14 @@
 // instead of once per sequence, and the product is a real matrix product for tcgen05.
 //
 // gdn_tile_attn_kernel -- one CTA = up to 256 query rows (row tiles A and B of 128) x a range of 128-key
-// tiles of one key/value head.  Warp 8 loads K and V tiles page by page by TMA into a ring, warp 9 issues the
-// MMAs and cleans V rows that must not be seen; warps 0-3 and 4-7 are the softmax of A and B (thread = row =
-// TMEM lane).  The tensor pipe runs S = Q K^T and O += P V of one row tile while the other's softmax runs: S_A,
-// S_B, then per key tile P_A V, S_A(next), P_B V, S_B(next).  P (bf16) overwrites S from its first columns on;
-// S(next) waits for the product that reads P, so a thread that sees S(next) may also rescale O.  160 KB of shared
-// memory and 80 registers a thread leave room on the SM for a CTA of the other kernel, whose loads fill
-// the time in which this one computes.
+// tiles of one key/value head.  Warp 16 loads K and V tiles page by page by TMA into a ring, warp 17 issues
+// S = Q K^T, warp 19 cleans V rows that must not be seen and issues O += P V; warps 0-7 and 8-15 are the softmax of
+// A and B.  A row (TMEM lane) has two threads, each with 64 of a tile's 128 scores: they share the maximum only
+// when it moves.  S_A and S_B take turns in the same TMEM columns, which are free as soon as the scores are in
+// registers; P (bf16) has columns of its own per row tile, so S(next) runs while this tile's exponentials
+// do.  Bound by the exponential unit and the shared memory reads of the products together: 256 requests of 4
+// query heads per key/value head over 16384 prefix keys take 75 us where the products alone are 40 us of the tensor
+// pipe's measured rate and the exponentials 30 us.
 //
 // gdn_warp_attn_kernel -- few query rows of a key list (L (H / H_kv) <= 16: a decode step): bound by
 // reading K and V, and a 128-row tile would be padding.  One CTA = (key list, key/value head, split),
@@ -52,9 +53,12 @@ using namespace sm100;
 
 constexpr int kTile = 128;                     // keys of a tile, rows of a row tile
 constexpr int kRows = 2 * kTile;               // rows of a CTA
-constexpr int kStages = 3;                     // K and V tiles in flight (four and five changed nothing)
-constexpr int kTThreads = 320;                 // eight softmax warps, loads, MMAs
-constexpr int kTRegs = 80;                     // with 160 KB of shared memory: leaves room for a CTA of few rows
+constexpr int kStages = 5;                     // K and V tiles in flight
+constexpr int kTThreads = 640;                 // 16 softmax warps, load, S, idle, P V (register shares go by four warps)
+// Registers a thread: the launch gives 96 (65536 / 640, in eights); the softmax warps hold half a row of
+// S and take what the load and MMA warps give up.
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 104, kRegsOther = 56;
+static_assert(4 * kRegsSoftmax + kRegsOther <= 5 * kRegsLaunch, "a warpgroup would wait for registers for ever");
 constexpr int kWKeys = 64;                     // gdn_warp_attn_kernel: keys of a tile (16 per warp)
 constexpr int kWThreads = 160;                 // four warps of arithmetic and one that loads
 constexpr int kWRows = 16;                     // most query rows
@@ -170,7 +174,7 @@ struct Item {
 // all started.  The first kernel of a call waits for the work before it (the inputs, an earlier call's use of the
 // workspace) and only then lets the next one start, so the second kernel may read inputs and write its parts at
 // once.  The combine kernel waits for the second kernel, whose last CTA waits for the first one before it ends (if
-// every CTA did, those that share an SM with the first kernel could not make room for the next ones).
+// every CTA did, the first ones to be done would keep their SMs from those that have not started).
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_end() {
@@ -221,45 +225,59 @@ __device__ __forceinline__ int64_t row_of(const PrefixParams &P, int hk, int row
     return (int64_t)nl * P.H + hk * P.G + (row - nl * P.G);
 }
 
-// 32 columns of a row of S, x, to P = 2^(x scale - mu) as 16 bf16 pairs; adds P to sum.  Bound by the exponential unit
-// (8 clocks a warp instruction); taking a share of the exponentials as polynomials on the FMA pipe gained nothing.
-__device__ __forceinline__ void softmax_chunk(const float (&x)[32], f2 scale2, f2 shift2, uint32_t (&pk)[16], f2 (&sum)[2]) {
+// Half a row of S, x (-inf where a key is not visible), to P = 2^(x scale - m_ref) as bf16 pairs in the TMEM
+// columns [tp, tp + 32), which may be written once free() has returned: ls = the sum of P, mt = the largest
+// x in log2 units.  Bound by the exponential unit (8 clocks a warp instruction); taking a share of the
+// exponentials as polynomials on the FMA pipe gained nothing.
+template <typename FREE>
+__device__ __forceinline__ void softmax_half(const float (&x)[2][32], float scale, float m_ref, uint32_t tp, float &ls,
+                                             float &mt, const FREE &free) {
+    const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+    const f2 scale2 = f2_of(scale, scale), shift2 = f2_of(-mu, -mu);
+    f2 sum[4] = {0, 0, 0, 0};
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        float p0, p1;
-        f2_get(f2_fma(f2_of(x[2 * e], x[2 * e + 1]), scale2, shift2), p0, p1);
-        p0 = ex2_approx(p0);
-        p1 = ex2_approx(p1);
-        sum[e & 1] = f2_add(sum[e & 1], f2_of(p0, p1));
-        pk[e] = pack_bf2(p0, p1);
+    for (int c = 0; c < 2; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float x0 = x[c][2 * e], x1 = x[c][2 * e + 1];
+            mx[e & 3] = fmaxf(mx[e & 3], fmaxf(x0, x1));
+            float p0, p1;
+            f2_get(f2_fma(f2_of(x0, x1), scale2, shift2), p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            sum[e & 3] = f2_add(sum[e & 3], f2_of(p0, p1));
+            pk[e] = pack_bf2(p0, p1);
+        }
+        if (c == 0) free();
+        tmem_st16(tp + 16 * c, pk);
     }
+    float ls1;
+    f2_get(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), ls, ls1);
+    ls += ls1;
+    mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
 }
 
 struct PrefixMaps {
     CUtensorMap k, v;                          // [P p, H_kv, d], box: 64 columns x 1 head x min(p, 64) rows
 };
 
-// Barriers and words of a tile CTA, behind its tiles in the dynamic shared memory.
-struct TileCtrl {
-    uint64_t full[kStages], empty[kStages];
-    uint64_t bar_s[2], bar_p[2], bar_v[2], bar_o[2], bar_drain;    // S complete, P written, P V done, O complete
-    uint32_t tmem;
-    int abort, status;
-};
-
 template <int D>
-__global__ void __maxnreg__(kTRegs)
+__global__ void __launch_bounds__(kTThreads, 1)
 gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ PrefixMaps M) {
     constexpr int kHalves = D / 64;
     constexpr int kTileBytes = kTile * D * 2;
-    constexpr uint32_t T_S = 0, T_O = 256;     // TMEM columns: S of A, S of B, O of A, O of B (128 apart)
-    extern __shared__ uint8_t smraw[];         // no static part: it starts on a 1024-byte boundary (checked below)
-    uint8_t *sm_q = smraw, *sm_kv = sm_q + 2 * kTileBytes;
-    TileCtrl &ctrl = *reinterpret_cast<TileCtrl *>(sm_kv + kStages * kTileBytes);
-    uint64_t *full = ctrl.full, *empty = ctrl.empty, *bar_s = ctrl.bar_s, *bar_p = ctrl.bar_p, *bar_v = ctrl.bar_v, *bar_o = ctrl.bar_o;
-    uint64_t &bar_drain = ctrl.bar_drain;
-    uint32_t &s_tmem = ctrl.tmem;
-    int &s_abort = ctrl.abort, &s_status = ctrl.status;
+    constexpr uint32_t T_S = 0, T_P = 128, T_O = 256;    // TMEM columns: S; P of A and B (64 apart); O of A and B (128 apart)
+    extern __shared__ uint8_t smraw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sm_q = sm, *sm_kv = sm + 2 * kTileBytes;
+    __shared__ uint64_t full[kStages], empty[kStages];
+    // S of A / B is complete; it is in registers; P of A / B is written; P V is done
+    __shared__ uint64_t bar_s[2], bar_r[2], bar_p[2], bar_o[2], bar_drain[2];
+    __shared__ float s_pair[kRows];            // between a row's two threads: maxima, at the end a sum
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort, s_status;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int item = P.first_item + blockIdx.x;
@@ -269,34 +287,38 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
     const Item w = item_of<kTile, kRows, 1>(P, item);
     const int tiles = w.t1 - w.t0;
     float2 *ml = P.part_ml + w.part * P.rows;
-    const bool askew = smem_u32(smraw) & 1023u;            // the tiles' swizzle needs the boundary
-    if (tiles == 0 || askew) {                 // an empty part: nothing visible
+    if (tiles == 0) {                          // an empty part: nothing visible
         for (int r = tid; r < w.nrows; r += kTThreads) ml[row_of(P, w.hk, w.row0 + r)] = make_float2(-INFINITY, 0.f);
-        if (tid == 0) P.item_status[item] = askew ? (int)GDN_ERR_TIMEOUT | 99 << 16 : 0;
+        if (tid == 0) P.item_status[item] = 0;
         grid_end();
         return;
     }
     const int two = w.nrows > kTile;           // row tile B is in use
 
-    // The ring's order is the order of use: K0 V0 K1 V1 ...  Loads tile i of the ring (warp 8): lane = (half, box), a
-    // box is min(p, 64) rows of one page, 64 columns; rows past the end read as zeros.
+    // The ring's order is the order of use: K0 K1 V0 K2 V1 ... V(last).  Loads tile i of the ring (warp 16):
+    // lane = (half, box), a box is min(p, 64) rows of one page, 64 columns; rows past the end read as zeros.
+    auto v_at = [&](int j) { return j + 1 < tiles ? 2 * j + 2 : 2 * j + 1; };
     const int box_rows = min(P.page, 64), boxes = kTile / box_rows, box = lane % boxes, half_of = lane / boxes;
-    // This lane's cache row in the current key tile, for K and again for V; the next tile's page ids are on their way.
-    int id_next = -1, row = 0;
+    // This lane's cache row in key tile j, for K and again for V; the page ids of the tile after are on their way.
+    int id_next = -1, rows_of[2] = {0, 0};
     auto fetch_id = [&](int j) {
         const int key = (w.t0 + j) * kTile + box * box_rows;
         id_next = half_of < kHalves && j < tiles && key < w.keys ? w.list[key / P.page] : -2;
     };
     auto load = [&](int i) {
-        const int j = i >> 1, slot = i % kStages;
-        const bool value = i & 1;
+        const bool value = i > 0 && ((i & 1) == 0 || i == 2 * tiles - 1);
+        const int j = value ? (i == 2 * tiles - 1 ? tiles - 1 : i / 2 - 1) : (i + 1) / 2;
+        const int slot = i % kStages;
         if (!value) {
             const int id = id_next;
-            row = P.pages * P.page;            // past the end: reads as zeros
+            int row = P.pages * P.page;        // past the end: reads as zeros
             if (id >= 0 && id < P.pages) row = id * P.page + ((w.t0 + j) * kTile + box * box_rows) % P.page;
             else if (id != -2) atomicOr(&s_status, (int)GDN_ERR_INVALID_ARG);
+            if (j & 1) rows_of[1] = row;
+            else rows_of[0] = row;
             fetch_id(j + 1);
         }
+        const int row = j & 1 ? rows_of[1] : rows_of[0];
         if (lane == 0) mbar_arrive_expect_tx(&full[slot], kTileBytes);
         __syncwarp();
         if (half_of < kHalves)
@@ -304,7 +326,7 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
                         &full[slot], half_of * 64, w.hk, row);
         __syncwarp();
     };
-    if (warp == 8) {
+    if (warp == 16) {
         fetch_id(0);
         if (lane == 0) {
             for (int i = 0; i < kStages; ++i) {
@@ -313,24 +335,24 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&bar_s[i], 1);
-                mbar_init(&bar_p[i], 4);
-                mbar_init(&bar_v[i], 1);
+                mbar_init(&bar_r[i], 8);
+                mbar_init(&bar_p[i], 8);
                 mbar_init(&bar_o[i], 1);
+                mbar_init(&bar_drain[i], 1);
             }
-            mbar_init(&bar_drain, 1);
             fence_mbar_init();
             fence_async_smem();
             s_abort = s_status = 0;
         }
         __syncwarp();
         for (int i = 0; i < min(kStages, 2 * tiles); ++i) load(i);         // beside the queries' loads
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         tmem_alloc(&s_tmem, 512);
         tmem_relinquish();
-    } else if (warp < 8) {
-        // queries: D / 8 chunks of 16 bytes a row, a pass covers 256 / (D / 8) rows; asynchronous copies in a short
+    } else if (warp < 16) {
+        // queries: D / 8 chunks of 16 bytes a row, a pass covers 512 / (D / 8) rows; asynchronous copies in a short
         // loop (a launch starts with cold instruction caches); rows past the last are zeros
-        constexpr int kChunks = D / 8, kPass = 256 / kChunks;
+        constexpr int kChunks = D / 8, kPass = 512 / kChunks;
         const int c = tid % kChunks;
         int r = tid / kChunks;
         int nl = (w.row0 + r) / P.G, g = (w.row0 + r) - nl * P.G;         // (n, l) and head of the row
@@ -354,8 +376,8 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
     const uint32_t tb = s_tmem;
 
     // Bounded wait.  A wait that gives up marks the CTA as stopping and returns; every further wait gives up at
-    // once.  Loads and products stop at the end of the key tile; the softmax warps run through their tiles (on
-    // unspecified data) and write nothing.
+    // once.  Loads and products stop at the end of the key tile; the softmax warps, which meet at the barriers of
+    // their pairs, run through their tiles (on unspecified data) and write nothing.
     auto stopped = [&] { return *reinterpret_cast<volatile int *>(&s_abort) != 0; };
     auto wait = [&](uint64_t *bar, uint32_t parity, int where) {
         if (mbar_try_wait(bar, parity)) return;
@@ -365,11 +387,12 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
         }
         if (atomicExch(&s_abort, 1) == 0) atomicExch(&s_status, (int)GDN_ERR_TIMEOUT | where << 16);
     };
-    // keys from this one on are not for every query row
+    // V rows from key `newest` on are not for every query row (see the file comment): warp 19 cleans their tiles
     const int newest = (w.n >= 0 && P.causal) ? w.keys - (P.L - 1) : w.keys;
 
-    if (warp == 8) {
+    if (warp == 16) {
         // ---------------------------------------------------------------- loads
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         int issued = min(kStages, 2 * tiles);
         for (; issued < 2 * tiles; ++issued) {
             wait(&empty[issued % kStages], (issued / kStages - 1) & 1, 1);
@@ -380,113 +403,120 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
         if (__any_sync(0xffffffffu, stopped()) && lane == 0)   // gave up: the loads in flight still land
             for (int i = max(0, issued - kStages); i < issued; ++i)
                 mbar_wait(&full[i % kStages], (i / kStages) & 1, kDrainWaitIters);
-    } else if (warp == 9) {
-        // ---------------------------------------------------------------- products
-        // Warp-uniform, with few instructions between the products: a single thread's chain of address arithmetic
-        // and branches cost more than the products that it fed.
-        constexpr uint32_t idesc_s = make_idesc_bf16(128, 128, 0, 0);
-        constexpr uint32_t idesc_o = make_idesc_bf16(128, D, 0, 1);
+    } else if (warp == 17 || warp == 19) {
+        // ---------------------------------------------------------------- products: S (warp 17), P V (warp 19)
+        // Two streams, so that one's products run while the other waits on a barrier; warp-uniform, with few
+        // instructions between the products (a single thread's chain of address arithmetic and branches
+        // cost more than the products that it fed).
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         constexpr uint32_t kStep = kTileBytes >> 4;
-        const uint64_t dq = make_sdesc(smem_u32(sm_q), 16, 1024), dk = make_sdesc(smem_u32(sm_kv), 16, 1024);
-        const uint64_t dv = make_sdesc(smem_u32(sm_kv), kTile * 128, 1024);
-        auto score = [&](int t, int slot) {    // S_t = Q_t K^T
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
-                mma_bf16(tb + T_S + 128 * t, dq + t * kStep + off, dk + slot * kStep + off, idesc_s, kk > 0);
-            }
-            mma_commit(&bar_s[t]);
-            if (t == two) mma_commit(&empty[slot]);
-        };
-        // V rows of the list from key `newest` on are not for every query row (see the file comment)
-        auto clean = [&](int slot, int key0) {
-                uint8_t *v = sm_kv + slot * kTileBytes;
-                const int last = min(kTile, w.keys - key0);          // rows [last, 128) are behind the list's end
-                for (int i = lane; i < (kTile - last) * (D / 8); i += 32) {
-                    const int r = last + i / (D / 8), c = i % (D / 8);
-                    *reinterpret_cast<uint4 *>(v + (c >> 3) * (kTile * 128) + sw128_off(r, c & 7)) = make_uint4(0, 0, 0, 0);
-                }
-                const int lo = max(newest - key0, 0);                // rows [lo, last) are visible to some rows only
-                bool found = false;
-                for (int i = lane; i < (last - lo) * (D / 8); i += 32) {
-                    const int r = lo + i / (D / 8), c = i % (D / 8);
-                    uint32_t *p = reinterpret_cast<uint32_t *>(v + (c >> 3) * (kTile * 128) + sw128_off(r, c & 7));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t x = p[e];
-                        const bool a = (x & 0x7f80u) == 0x7f80u, b = (x & 0x7f800000u) == 0x7f800000u;
-                        if (a) x &= 0xffff0000u;
-                        if (b) x &= 0xffffu;
-                        if (a || b) {
-                            p[e] = x;
-                            found = true;
-                        }
-                    }
-                }
-                if (found) atomicOr(&s_status, kItemNonfinite);
-                fence_async_smem();
-                __syncwarp();
-        };
-        int slot = 0;
+        int slot = 0, left = tiles;
         uint32_t phase = 0;
-        auto take = [&](int where) {           // the next tile of the ring
-            const int s = slot;
-            wait(&full[s], phase, where);
-            if (++slot == kStages) slot = 0, phase ^= 1;
-            return s;
+        auto advance = [&](int n) {            // n tiles on in the ring
+            slot += n;
+            if (slot >= kStages) slot -= kStages, phase ^= 1;
         };
-        int k = take(2);
-        tc_fence_after();
-        if (elect_one()) {
-            score(0, k);
-            if (two) score(1, k);
-        }
-        __syncwarp();
-        int end = (w.t0 + 1) * kTile;
-        for (int j = 0; j < tiles; ++j, end += kTile) {
-            const bool next = j + 1 < tiles;
-            const int v = take(3);
-            if (end > newest) clean(v, end - kTile);               // while the softmax is at work
-            if (next) k = take(5);
-            for (int t = 0; t <= two; ++t) {
-                wait(&bar_p[t], j & 1, 6);
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)               // O_t (+)= P_t V
-                        mma_bf16_ts(tb + T_O + 128 * t, tb + T_S + 128 * t + kk * 8, dv + v * kStep + kk * 128, idesc_o, j > 0 || kk > 0);
-                    mma_commit(&bar_v[t]);
-                    if (t == two) mma_commit(&empty[v]);
-                    if (!next) mma_commit(&bar_o[t]);
-                }
-                __syncwarp();
-                // S(next) is written over P: products with different accumulators are not ordered by themselves
-                wait(&bar_v[t], j & 1, 5);
-                if (next) {
+        if (warp == 17) {
+            constexpr uint32_t idesc = make_idesc_bf16(128, 128, 0, 0);
+            const uint64_t dq = make_sdesc(smem_u32(sm_q), 16, 1024), dk = make_sdesc(smem_u32(sm_kv), 16, 1024);
+            uint32_t odd = 0;                  // parity of the key tile
+            for (int j = 0; j < tiles; ++j, odd ^= 1) {
+                wait(&full[slot], phase, 2);
+                for (int t = 0; t <= two; ++t) {
+                    // the S before this one (of the other row tile, or of this one) is in registers
+                    if (t == 1) wait(&bar_r[0], odd, 3);
+                    else if (j > 0) wait(&bar_r[two], odd ^ 1, 3);
                     tc_fence_after();
-                    if (elect_one()) score(t, k);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
+                            mma_bf16(tb + T_S, dq + t * kStep + off, dk + slot * kStep + off, idesc, kk > 0);
+                        }
+                        mma_commit(&bar_s[t]);
+                        if (t == two) mma_commit(&empty[slot]);
+                    }
                     __syncwarp();
                 }
+                advance(j == 0 ? 1 : 2);
+                if (__any_sync(0xffffffffu, stopped())) break;
             }
-            if (__any_sync(0xffffffffu, stopped())) break;
+        } else {
+            constexpr uint32_t idesc = make_idesc_bf16(128, D, 0, 1);
+            const uint64_t dv = make_sdesc(smem_u32(sm_kv), kTile * 128, 1024);
+            int end = (w.t0 + 1) * kTile;
+            slot = tiles > 1 ? 2 : 1;
+            for (int j = 0; j < tiles; ++j, end += kTile) {
+                wait(&full[slot], phase, 4);
+                if (end > newest) {
+                    const int key0 = end - kTile;
+                    uint8_t *v = sm_kv + slot * kTileBytes;
+                    const int last = min(kTile, w.keys - key0);          // rows [last, 128) are behind the list's end
+                    for (int i = lane; i < (kTile - last) * (D / 8); i += 32) {
+                        const int r = last + i / (D / 8), c = i % (D / 8);
+                        *reinterpret_cast<uint4 *>(v + (c >> 3) * (kTile * 128) + sw128_off(r, c & 7)) = make_uint4(0, 0, 0, 0);
+                    }
+                    const int lo = max(newest - key0, 0);                // rows [lo, last) are visible to some rows only
+                    bool found = false;
+                    for (int i = lane; i < (last - lo) * (D / 8); i += 32) {
+                        const int r = lo + i / (D / 8), c = i % (D / 8);
+                        uint32_t *p = reinterpret_cast<uint32_t *>(v + (c >> 3) * (kTile * 128) + sw128_off(r, c & 7));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t x = p[e];
+                            const bool a = (x & 0x7f80u) == 0x7f80u, b = (x & 0x7f800000u) == 0x7f800000u;
+                            if (a) x &= 0xffff0000u;
+                            if (b) x &= 0xffffu;
+                            if (a || b) {
+                                p[e] = x;
+                                found = true;
+                            }
+                        }
+                    }
+                    if (found) atomicOr(&s_status, kItemNonfinite);
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                for (int t = 0; t <= two; ++t) {
+                    wait(&bar_p[t], j & 1, 6);
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_bf16_ts(tb + T_O + 128 * t, tb + T_P + 64 * t + kk * 8, dv + slot * kStep + kk * 128, idesc, j > 0 || kk > 0);
+                        mma_commit(&bar_o[t]);
+                        if (t == two) mma_commit(&empty[slot]);
+                    }
+                    __syncwarp();
+                }
+                advance(--left > 1 ? 2 : 1);   // the last V follows the one before it
+                if (__any_sync(0xffffffffu, stopped())) break;
+            }
         }
         if (__any_sync(0xffffffffu, stopped()) && elect_one()) {       // gave up: the MMAs in flight still end
-            mma_commit(&bar_drain);
-            mbar_wait(&bar_drain, 0, kDrainWaitIters);
+            mma_commit(&bar_drain[warp == 19]);
+            mbar_wait(&bar_drain[warp == 19], 0, kDrainWaitIters);
         }
         __syncwarp();
+    } else if (warp > 16) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     } else {
         // ---------------------------------------------------------------- softmax
-        const int t = warp >> 2, quad = warp & 3, r = tid;                     // row of the CTA = thread
-        const bool live = r < w.nrows, warp_live = (warp << 5) < w.nrows;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        const int t = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3;
+        const int r = t * kTile + quad * 32 + lane;                            // row of the CTA
+        const int pair = 1 + t * 4 + quad;                                     // named barrier of the rows' two warps
+        const bool live = r < w.nrows;
+        const bool warp_live = t * kTile + quad * 32 < w.nrows;
         // keys [0, sees) are this row's
         int sees = live ? w.keys : 0;
         if (live && w.n >= 0 && P.causal) {
             const int l = ((w.row0 + r) / P.G) % P.L;
             sees = max(0, w.keys - (P.L - 1 - l));
         }
-        const uint32_t ts = tmem_addr(tb, quad * 32, T_S + 128 * t);      // S, then P over what has been read of it
-        const uint32_t to = tmem_addr(tb, quad * 32, T_O + 128 * t);
+        const uint32_t ts = tmem_addr(tb, quad * 32, T_S + 64 * half);                     // this thread's half of S,
+        const uint32_t tp = tmem_addr(tb, quad * 32, T_P + 64 * t + 32 * half);            // of P
+        const uint32_t to = tmem_addr(tb, quad * 32, T_O + 128 * t + (D / 2) * half);      // and of O
         const float sl2 = P.scale_log2;
         float m_ref = -INFINITY, l_sum = 0.f;
         if (t == 0 || two) {
@@ -494,109 +524,130 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
                 wait(&bar_s[t], j & 1, 7);
                 __syncwarp();
                 tc_fence_after();
+                float x[2][32];
                 if (warp_live) {
-                    const int hi = sees - (w.t0 + j) * kTile;    // columns [0, hi) are visible
-                    const bool whole = __all_sync(0xffffffffu, hi >= kTile);
-                    float x[2][32];
-                    // the row's max, 64 columns at a time (S is read twice: a row in registers would not leave
-                    // room on the SM for another CTA)
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                    for (int c0 = 0; c0 < kTile; c0 += 64) {
-                        tmem_ld32(ts + c0, x[0]);
-                        tmem_ld32(ts + c0 + 32, x[1]);
-                        tmem_wait_ld();
-                        if (!whole) {
+                    tmem_ld32(ts, x[0]);
+                    tmem_ld32(ts + 32, x[1]);
+                    tmem_wait_ld();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar_r[t]);           // S may be overwritten
+                // P V of the tile before is done: P may be overwritten, O rescaled
+                bool waited = j == 0;
+                auto free = [&] {
+                    if (!waited) {
+                        wait(&bar_o[t], (j - 1) & 1, 8);
+                        __syncwarp();
+                        tc_fence_after();
+                        waited = true;
+                    }
+                };
+                if (warp_live) {
+                    const int hi = sees - (w.t0 + j) * kTile - 64 * half;      // this half's columns [0, hi) are visible
+                    if (hi < 64) {
 #pragma unroll
-                            for (int e = 0; e < 64; ++e) x[e / 32][e % 32] = c0 + e < hi ? x[e / 32][e % 32] : -INFINITY;
-                        }
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[c][e] = 32 * c + e < hi ? x[c][e] : -INFINITY;
+                    }
+                    // P = 2^(s - m) with the reference max of the tiles before, while the tile's own max is
+                    // taken beside it (it would wait for itself in a pass of its own).  Only if that max
+                    // passes the reference by more than the margin is m moved, O and l rescaled and P taken
+                    // again, which is rare.  The rows' two warps decide together.
+                    float ls;
+                    if (j == 0) {              // no reference yet: the row's max first, through its two threads
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                         for (int e = 0; e < 64; e += 2) mx[e / 2 & 3] = fmaxf(mx[e / 2 & 3], fmaxf(x[e / 32][e % 32], x[e / 32][e % 32 + 1]));
+                        float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                        if (half == 0) s_pair[r] = mt;
+                        asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+                        if (half == 1) s_pair[r] = mt = fmaxf(mt, s_pair[r]);
+                        asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+                        m_ref = s_pair[r];
                     }
-                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-                    // The reference max moves, and O and l are rescaled, only past the margin
-                    const bool up = mt > m_ref + kMargin;
-                    if (__any_sync(0xffffffffu, up)) {
+                    while (true) {
+                        float mt;
+                        softmax_half(x, sl2, m_ref, tp, ls, mt, free);
+                        if (!bar_sync_or(pair, 64, mt > m_ref + kMargin)) break;
+                        if (half == 0) s_pair[r] = mt;
+                        asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+                        if (half == 1) s_pair[r] = mt = fmaxf(mt, s_pair[r]);
+                        asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+                        mt = s_pair[r];
+                        const bool up = mt > m_ref + kMargin;
                         const float alpha = !up ? 1.f : m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - mt);
                         if (up) m_ref = mt;
                         l_sum *= alpha;
+                        tmem_wait_st();
                         if (j > 0) {
 #pragma unroll 1
-                            for (int c0 = 0; c0 < D; c0 += 32) {
-                                tmem_ld32(to + c0, x[0]);
+                            for (int c0 = 0; c0 < D / 2; c0 += 32) {
+                                float o[32];
+                                tmem_ld32(to + c0, o);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) x[0][e] *= alpha;
-                                tmem_st32(to + c0, x[0]);
+                                for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                                tmem_st32(to + c0, o);
                             }
                         }
                     }
-                    const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-                    const f2 scale2 = f2_of(sl2, sl2), shift2 = f2_of(-mu, -mu);
-                    f2 sum[2] = {0, 0};
-                    tmem_ld32(ts, x[0]);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_wait_ld();
-                        if (c < 3) tmem_ld32(ts + 32 * (c + 1), x[(c + 1) & 1]);
-                        float(&y)[32] = x[c & 1];
-                        if (!whole) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) y[e] = 32 * c + e < hi ? y[e] : -INFINITY;
-                        }
-                        uint32_t pk[16];
-                        softmax_chunk(y, scale2, shift2, pk, sum);
-                        tmem_st16(ts + 16 * c, pk);
-                    }
-                    float l0, l1;
-                    f2_get(f2_add(sum[0], sum[1]), l0, l1);
-                    l_sum += l0 + l1;
+                    l_sum += ls;
                     tmem_wait_st();
+                } else {
+                    free();
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar_p[t]);
             }
-            wait(&bar_o[t], 0, 8);
+            wait(&bar_o[t], (tiles - 1) & 1, 10);
             __syncwarp();
-            if (warp_live && !__any_sync(0xffffffffu, stopped())) {
+            if (warp_live && !bar_sync_or(pair, 64, stopped())) {
                 tc_fence_after();
+                if (half == 1) s_pair[r] = l_sum;
+                asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
                 const int64_t row = live ? row_of(P, w.hk, w.row0 + r) : 0;
-                if (m_ref == -INFINITY && l_sum != 0.f) m_ref = 0.f;           // every visible score is NaN: so is the row
-                if (live) ml[row] = make_float2(m_ref, l_sum);
+                if (live && half == 0) {
+                    l_sum += s_pair[r];
+                    if (m_ref == -INFINITY && l_sum != 0.f) m_ref = 0.f;       // every visible score is NaN: so is the row
+                    ml[row] = make_float2(m_ref, l_sum);
+                }
                 // O leaves row by row through shared memory (a lane holds a row: 32 rows at once would be 32
-                // partial lines per store), 64 columns at a time, in the space of this row tile's queries, whose
-                // products are done.
-                float4 *st = reinterpret_cast<float4 *>(sm_q + t * kTileBytes) + quad * 32 * (D / 8);
+                // partial lines per store), in the space of this row tile's queries, whose products are done.  It
+                // holds 64 columns of the tile: one half after the other at d = 128.
                 constexpr int kC = D / 8;                        // 16-byte chunks of half a row, chunk c at c ^ (row & 7)
-                const int chunks = min(32, w.nrows - (warp << 5)) * kC;
-#pragma unroll 1
+                float4 *st = reinterpret_cast<float4 *>(sm_q + t * kTileBytes) + quad * 32 * kC;
+                const int rows = min(32, w.nrows - (t * kTile + quad * 32));
                 for (int h = 0; h < 2; ++h) {
+                    if (half == h) {
 #pragma unroll 1
-                    for (int c0 = 0; c0 < D / 2; c0 += 32) {
-                        float o[32];
-                        tmem_ld32(to + h * (D / 2) + c0, o);
-                        tmem_wait_ld();
+                        for (int c0 = 0; c0 < D / 2; c0 += 32) {
+                            float o[32];
+                            tmem_ld32(to + c0, o);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            st[lane * kC + (((c0 + e) / 4) ^ (lane & 7))] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            for (int e = 0; e < 32; e += 4)
+                                st[lane * kC + (((c0 + e) / 4) ^ (lane & 7))] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        }
                     }
-                    __syncwarp();
+                    asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
 #pragma unroll 4
-                    for (int i0 = 0; i0 < chunks; i0 += 32) {
+                    for (int i0 = half * 32; i0 < rows * kC; i0 += 64) {
                         const int i = i0 + lane, rr = min(i / kC, 31), c = i % kC;
                         const int64_t dst = __shfl_sync(0xffffffffu, row, rr);
-                        if (i < chunks)
+                        if (i < rows * kC)
                             reinterpret_cast<float4 *>(P.part_o + (w.part * P.rows + dst) * D + (D / 2) * h)[c] = st[rr * kC + (c ^ (rr & 7))];
                     }
-                    __syncwarp();
+                    asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
                 }
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) tmem_dealloc(tb, 512);
+    if (warp == 17) tmem_dealloc(tb, 512);
     if (tid == 0) P.item_status[item] = s_status;
     grid_end();
 }
@@ -622,10 +673,9 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Tiles on their way and CTAs that share an SM: at d = 128 and one column tile of rows three CTAs of two tiles (64
-// KB each) beat two of three, because one CTA's start lies behind two others' loads (own keys of 64
-// requests of up to 1024 tokens: 35 against 40 us); elsewhere registers allow two CTAs, or tiles are
-// small.
+// Tiles on their way: at d = 128 three CTAs an SM of two tiles (64 KB each, 136 registers a thread) beat two CTAs of
+// three, because one CTA's start lies behind two others' loads (own keys of 64 requests of up to 1024
+// tokens, 32 query heads on 8: 35 against 40 us; of 32 requests with 4 tokens each, 47 against 61 us).
 template <int D, int NT>
 constexpr int warp_stages() { return D == 128 ? 2 : 3; }
 template <int D, int NT>
@@ -633,7 +683,7 @@ constexpr int warp_smem() { return warp_stages<D, NT>() * 2 * kWKeys * D * 2 + 1
 
 // NT: column tiles of 8 rows.
 template <int D, int NT>
-__global__ void __maxnreg__(112)
+__global__ void __maxnreg__(136)
 gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ PrefixMaps M) {
     constexpr int kHalves = D / 64;
     constexpr int kHalfBytes = kWKeys * 128;
@@ -1067,18 +1117,17 @@ struct Plan {
 };
 
 // Splits of `tiles` key tiles over `base` equal lists for gdn_tile_attn_kernel, beside other work of `beside`
-// SM-microseconds in the same call.  A CTA takes tile_us a key tile and kStartUs for its start and end (measured at
-// two row tiles, d = 128: 2.25, or 2.7 beside other CTAs' loads, and 12.7); the call takes as long as its waves of CTAs, or as all its work on all
+// SM-microseconds in the same call.  A CTA has an SM to itself and takes kTileUs a key tile and kStartUs for its start and
+// end (measured at two row tiles, d = 128); the call takes as long as its waves of CTAs, or as all its work on all
 // SMs, and each part a little in the combine step.  With own keys beside it a prefix is thus cut into fewer
-// parts than would fill the GPU (8192 keys for 64 requests of up to 1024 own tokens: 8 parts, 48 us; 16
-// parts, 58 us).
+// parts than would fill the GPU: 16384 keys for 256 requests of up to 1024 own tokens, 3 parts of 32 CTAs
+// 110 us, 4 parts 123 us (2 parts 132 us); the prefix alone, 92 us and 75 us.
 int tile_split(int64_t base, int64_t tiles, double beside) {
-    constexpr double kStartUs = 12.7, kPartUs = 0.3;
-    const double tile_us = beside > 0.0 ? 2.7 : 2.25;
+    constexpr double kTileUs = 1.6, kStartUs = 12.0, kPartUs = 0.3;
     int best = 1;
     double cost = 1e300;
     for (int s = 1; s <= kMaxSplits && s <= tiles; ++s) {
-        const double cta = (double)((tiles + s - 1) / s) * tile_us + kStartUs;
+        const double cta = (double)((tiles + s - 1) / s) * kTileUs + kStartUs;
         const double waves = (double)((base * s + kSms - 1) / kSms) * cta;
         const double c = std::max(waves, ((double)(base * s) * cta + beside) / kSms) + kPartUs * s;
         if (c < cost * 0.999) cost = c, best = s;
@@ -1122,9 +1171,7 @@ Plan plan_of(const gdn_prefix_attn_desc *D) {
 }
 
 template <int D>
-constexpr int tile_smem() { return (2 + kStages) * kTile * D * 2 + (int)sizeof(TileCtrl); }
-// a tile CTA and a CTA of few rows share an SM: 228 KB, 1 KB of each CTA's own, static shared memory of the latter
-static_assert(tile_smem<128>() + 1024 + warp_smem<128, 1>() + 640 + 1024 <= 228 * 1024, "the two kernels would run one after the other");
+constexpr int tile_smem() { return (2 + kStages) * kTile * D * 2 + 1024; }
 
 // Raises the kernels' dynamic shared memory limits, once per device.
 template <int D>
@@ -1137,13 +1184,12 @@ cudaError_t prepare_device() {
     if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
     constexpr auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
     e = cudaFuncSetAttribute(gdn_tile_attn_kernel<D>, attr, tile_smem<D>());
+    // the shares that its warps take add up to what it is launched with, or they would wait for ever
+    cudaFuncAttributes fa;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, gdn_tile_attn_kernel<D>);
+    if (e == cudaSuccess && fa.numRegs < kRegsLaunch) e = cudaErrorInvalidConfiguration;
     if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_warp_attn_kernel<D, 1>, attr, warp_smem<D, 1>());
     if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_warp_attn_kernel<D, 2>, attr, warp_smem<D, 2>());
-    // the whole of the SM's memory as shared memory, or a CTA of the one kernel finds no room beside one of the other
-    constexpr auto carve = cudaFuncAttributePreferredSharedMemoryCarveout;
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_tile_attn_kernel<D>, carve, cudaSharedmemCarveoutMaxShared);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_warp_attn_kernel<D, 1>, carve, cudaSharedmemCarveoutMaxShared);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_warp_attn_kernel<D, 2>, carve, cudaSharedmemCarveoutMaxShared);
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
     return e;
 }
