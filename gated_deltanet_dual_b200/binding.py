@@ -681,20 +681,27 @@ def _cuda_index(t: torch.Tensor) -> int:
     return index
 
 
-def _call(name: str, index: int, stream, fresh, *args):
-    """Calls the library on device `index` and raises on an error.  Tensors that the caller allocated itself
-    (fresh) are kept alive for a stream that is not the current one."""
+def _fresh(shape, dtype, index: int, stream) -> torch.Tensor:
+    """A new tensor for a call on `stream`.  It is allocated there: memory that the current stream has freed may still
+    be written by work queued on it.  The current stream, where the caller may use it, is on its record too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+    current = torch.cuda.current_stream(index)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=index)):
+        t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+    if stream != current.cuda_stream:
+        t.record_stream(current)
+    return t
+
+
+def _call(name: str, index: int, stream, *args):
+    """Calls the library on device `index` and raises on an error."""
     fn = getattr(_lib or load_library(), name)
     if torch._C._cuda_getDevice() == index:
         st = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
     else:
         with torch.cuda.device(index):
             st = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
-    if stream is not None:
-        other = torch.cuda.ExternalStream(stream, device=index)
-        for t in fresh:
-            if t is not None:
-                t.record_stream(other)
     if st != GDN_OK:
         raise GdnError(st, f"{name} failed: {status_string(st)}")
 
@@ -757,13 +764,10 @@ def _rotary(name, q, k, positions, table, q_out, k_out, stream):
     H = q.shape[-2] if q is not None else 0
     Hkv = k.shape[-2] if k is not None else 0
     rows = T * (front[0] if len(front) == 2 else 1)
-    fresh = []
     if q is not None and q_out is None:
-        q_out = torch.empty(front + (H, d), dtype=io, device=lead.device)
-        fresh.append(q_out)
+        q_out = _fresh(front + (H, d), io, index, stream)
     if k is not None and k_out is None:
-        k_out = torch.empty(front + (Hkv, d), dtype=io, device=lead.device)
-        fresh.append(k_out)
+        k_out = _fresh(front + (Hkv, d), io, index, stream)
     strides = (_rows(q, "q", front + (H, d), io, index) + _rows(k, "k", front + (Hkv, d), io, index)
                + _rows(q_out if q is not None else None, "q_out", front + (H, d), io, index)
                + _rows(k_out if k is not None else None, "k_out", front + (Hkv, d), io, index))
@@ -771,7 +775,7 @@ def _rotary(name, q, k, positions, table, q_out, k_out, stream):
     turns = table._on(index)
     if rows and H + Hkv:
         desc = RotaryDesc(rows, T, H, Hkv, d, table._args[0], table._args[1], _dtype_code(lead), table._args[2], 0, *strides)
-        _call(name, index, stream, fresh, ctypes.byref(desc), turns, positions.data_ptr(), q.data_ptr() if H else None,
+        _call(name, index, stream, ctypes.byref(desc), turns, positions.data_ptr(), q.data_ptr() if H else None,
               k.data_ptr() if Hkv else None, q_out.data_ptr() if H else None, k_out.data_ptr() if Hkv else None)
     return q_out if q is not None else None, k_out if k is not None else None
 
@@ -831,7 +835,7 @@ def kv_extend(block_table, seq_lens, new_lens, free_pages, free_count, page_size
     if device_status is not None:
         _want(device_status, "device_status", (1,), i32, index)
     desc = KvExtendDesc(N, W, page_size, F, M, prefix_len, 0, 0)
-    _call("gdn_kv_extend", index, stream, (), ctypes.byref(desc), block_table.data_ptr(), seq_lens.data_ptr(),
+    _call("gdn_kv_extend", index, stream, ctypes.byref(desc), block_table.data_ptr(), seq_lens.data_ptr(),
           new_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), *tables._ptrs,
           None if device_status is None else device_status.data_ptr())
     return tables
@@ -847,10 +851,8 @@ def rotary_append(q, k, v, positions, slot_map, table: RotaryTable, k_cache, v_c
         raise ValueError("q, k, v and q_out must be [R, heads, d] and the caches [P, p, H_kv, d]")
     R, H, d = q.shape
     Hkv, (P, page) = k.shape[1], k_cache.shape[:2]
-    fresh = ()
     if q_out is None:
-        q_out = torch.empty(R, H, d, dtype=io, device=q.device)
-        fresh = (q_out,)
+        q_out = _fresh((R, H, d), io, index, stream)
     (qr, qh, q1), (kr, kh, k1), (vr, vh, v1), (outr, outh, out1) = q.stride(), k.stride(), v.stride(), q_out.stride()
     if not (q1 == k1 == v1 == out1 == 1 and k.shape[0] == R and k.shape[2] == d and v.shape == k.shape
             and q_out.shape == q.shape and k_cache.shape == v_cache.shape == (P, page, Hkv, d) and k.dtype is io
@@ -870,7 +872,7 @@ def rotary_append(q, k, v, positions, slot_map, table: RotaryTable, k_cache, v_c
         _want(device_status, "device_status", (1,), torch.int32, index)
     desc = AppendDesc(R, H, Hkv, d, table._args[0], table._args[1], page, P, _dtype_code(q), table._args[2],
                       qr, qh, kr, kh, vr, vh, outr, outh)
-    _call("gdn_rotary_append", index, stream, fresh, ctypes.byref(desc), table._on(index), positions.data_ptr(),
+    _call("gdn_rotary_append", index, stream, ctypes.byref(desc), table._on(index), positions.data_ptr(),
           slot_map.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), None if device_status is None else device_status.data_ptr())
     return q_out
@@ -916,22 +918,19 @@ def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len, block_table,
         _want(prefix_pages, "prefix_pages", (prefix_pages.numel(),), torch.int32, index)
         if prefix_len < 0 or prefix_pages.numel() < -(-prefix_len // page):
             raise ValueError(f"prefix_pages holds {prefix_pages.numel()} pages of {page} for {prefix_len} tokens")
-    fresh = ()
     if out is None:
-        out = torch.empty_like(q)
-        fresh = (out,)
+        out = _fresh(shape, io, index, stream)
     else:
         _want(out, "out", shape, io, index)
     desc = PrefixAttnDesc(N, L, H, Hkv, d, page, P, W, prefix_len, 1 if causal else 0, _dtype_code(q),
                           0.0 if scale is None else scale)
     if workspace is None:
-        ws = torch.empty(max(256, prefix_attn_workspace_size(desc)), dtype=torch.uint8, device=q.device)
-        fresh += (ws,)
+        ws = _fresh((max(256, prefix_attn_workspace_size(desc)),), torch.uint8, index, stream)
     else:
         ws = workspace.tensor
         if ws.get_device() != index:
             raise ValueError(f"workspace is on {ws.device}, expected cuda:{index}")
-    _call("gdn_prefix_attn", index, stream, fresh, ctypes.byref(desc), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+    _call("gdn_prefix_attn", index, stream, ctypes.byref(desc), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           prefix_pages.data_ptr() if prefix_len else None, block_table.data_ptr() if W else None, seq_lens.data_ptr(),
           out.data_ptr(), ws.data_ptr(), ws.numel())
     return out

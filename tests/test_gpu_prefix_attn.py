@@ -333,3 +333,27 @@ def test_every_call_gives_the_same_bits(N, L, H, Hkv, d, page, prefix, own):
     for _ in range(4000):
         wrong += (b.prefix_attention(**p, workspace=ws) != base).any()
     assert int(wrong) == 0 and b.read_device_status(ws) == b.GDN_OK
+
+
+def test_buffers_of_a_call_on_another_stream():
+    """A call on another stream takes no memory that queued work of the current stream still writes."""
+    p = _problem(4, 1, 8, 2, 128, 16, 300, [40] * 4, seed=14)
+    want = _run(p, True)
+    q, k = torch.randn(700, 8, 128, device="cuda"), torch.randn(700, 2, 128, device="cuda")
+    pos, table = torch.arange(700, device="cuda", dtype=torch.int32), b.rotary_table(128)
+    want_q, want_k = b.rotary_forward(q, k, pos, table)
+    side = torch.cuda.Stream()
+    a = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    freed = [[torch.empty_like(t) for _ in range(8)] for t in (want, want_q, want_k)]
+    for _ in range(20):
+        a @ a                                                                  # holds the writes below back
+    for like in freed:
+        for t in like:
+            t.fill_(float("nan"))
+    del t, like
+    freed.clear()
+    got = b.prefix_attention(**p, stream=side.cuda_stream)
+    got_q, got_k = b.rotary_forward(q, k, pos, table, stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(got_q, want_q) and torch.equal(got_k, want_k)
