@@ -1095,7 +1095,7 @@ bool desc_ok(const gdn_prefix_attn_desc *D) {
     return D && D->num_seqs >= 1 && D->num_tokens >= 1 && D->num_heads >= 1 && D->num_kv_heads >= 1 && D->head_dim >= 1 &&
            D->page_size >= 1 && D->num_pages >= 1 && D->table_width >= 0 && D->prefix_len >= 0 &&
            (D->causal == 0 || D->causal == 1) && (D->dtype == GDN_BF16 || D->dtype == GDN_FP32) &&
-           (D->scale == 0.f || (D->scale > 0.f && std::isfinite(D->scale))) && D->num_heads % D->num_kv_heads == 0 &&
+           (D->scale == 0.f || (D->scale > 0.f && std::isfinite(1.5f * D->scale))) && D->num_heads % D->num_kv_heads == 0 &&
            (int64_t)D->num_pages * D->page_size <= INT32_MAX && (int64_t)D->table_width * D->page_size <= INT32_MAX - kTile &&
            D->prefix_len <= INT32_MAX - kTile;
 }
@@ -1260,6 +1260,21 @@ extern "C" gdn_status gdn_prefix_attn(const gdn_prefix_attn_desc *D, const void 
     const Plan plan = plan_of(D);
     if (plan.prefix_items + plan.own_items > INT32_MAX) return GDN_ERR_UNSUPPORTED;
     if (workspace_bytes < plan.bytes) return GDN_ERR_INVALID_ARG;
+    struct Span {
+        uintptr_t lo, hi;
+        Span(const void *p, size_t n) : lo(reinterpret_cast<uintptr_t>(p)), hi(lo + (p ? n : 0)) {}
+        bool meets(const Span &o) const { return lo < o.hi && o.lo < hi; }
+    };
+    const size_t cache = (size_t)D->num_pages * D->page_size * D->num_kv_heads * D->head_dim * 2;
+    const size_t io = (size_t)plan.rows * D->head_dim * 2;
+    const Span written[] = {{out, io}, {workspace, plan.bytes}};
+    const Span read[] = {{q, io}, {k_cache, cache}, {v_cache, cache},
+                         {prefix_pages, ((size_t)D->prefix_len + D->page_size - 1) / D->page_size * 4},
+                         {block_table, (size_t)D->num_seqs * D->table_width * 4}, {seq_lens, (size_t)D->num_seqs * 4}};
+    if (written[0].meets(written[1])) return GDN_ERR_INVALID_ARG;
+    for (const Span &o : written)
+        for (const Span &i : read)
+            if (o.meets(i)) return GDN_ERR_INVALID_ARG;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     PrefixParams P = {};
     P.q = static_cast<const __nv_bfloat16 *>(q);

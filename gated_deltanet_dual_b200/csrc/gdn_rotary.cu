@@ -232,8 +232,7 @@ cudaError_t launch_rotary(const RotaryParams &P, bool vec, cudaStream_t st) {
 
 template <bool APPEND>
 gdn_status run_rotary(RotaryParams &P, int dtype, int interleaved, bool vec, cudaStream_t st) {
-    // Rows per CTA: one while that does not fill the GPU eight times over with 256-thread CTAs
-    // (a decode step wants every SM), else enough to share a CTA's set-up.
+    // Rows per CTA: one up to 16 CTAs a SM (a decode step wants every SM), else enough to share a CTA's set-up.
     P.rows_per_cta = (int)std::min<int64_t>(kRMaxRows, std::max<int64_t>(1, P.rows / (148 * 16)));
     cudaError_t e;
     if (dtype == GDN_BF16)
@@ -246,15 +245,37 @@ gdn_status run_rotary(RotaryParams &P, int dtype, int interleaved, bool vec, cud
 
 bool multiple(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// Strides of one tensor [rows, heads, d]: non-negative; an output's rows and heads must also lie
-// apart (each stride clears the extent of what is inside it, in either order).
+// Strides of one tensor [rows, heads, d]: non-negative, spanning less than 2^46 elements; an output's
+// rows and heads must also lie apart (each stride clears the extent of what is inside it, in either order).
 bool strides_ok(int64_t rs, int64_t hs, int64_t rows, int64_t heads, int64_t d, bool output) {
-    if (rs < 0 || hs < 0 || rs > (INT64_C(1) << 40) || hs > (INT64_C(1) << 40)) return false;
-    if (!output || rows == 0 || heads == 0) return true;
+    constexpr int64_t kMost = INT64_C(1) << 46;
+    if (rs < 0 || hs < 0) return false;
+    if (rows == 0 || heads == 0) return true;
+    if ((rows > 1 && rs > kMost / (rows - 1)) || (heads > 1 && hs > kMost / (heads - 1))) return false;
+    if (!output) return true;
     const bool heads_inside = (heads <= 1 || hs >= d) && (rows <= 1 || rs >= (heads - 1) * hs + d);
     const bool rows_inside = (rows <= 1 || rs >= d) && (heads <= 1 || hs >= (rows - 1) * rs + d);
     return heads_inside || rows_inside;
 }
+
+// The bytes of a tensor [rows, heads, d] (its strides have passed strides_ok).
+struct Cover {
+    uintptr_t lo;
+    int64_t rs, hs, row, all;                   // strides; bytes from a row's first element to its last, and of all rows
+    Cover(const void *p, int64_t rows, int64_t rs_, int64_t heads, int64_t hs_, int64_t d, int64_t e)
+        : lo(reinterpret_cast<uintptr_t>(p)), rs(rs_ * e), hs(hs_ * e), row(heads ? ((heads - 1) * hs_ + d) * e : 0),
+          all(p && rows && heads ? (rows - 1) * rs_ * e + row : 0) {}
+    Cover(const void *p, int64_t n, int64_t e) : Cover(p, 1, 0, 1, 0, n, e) {}
+    // No byte in common: one lies behind the other, or both have the same row stride and their rows alternate (slices
+    // of one projection's output).
+    bool apart(const Cover &o) const {
+        if (all == 0 || o.all == 0 || lo + all <= o.lo || o.lo + o.all <= lo) return true;
+        if (rs != o.rs || rs == 0 || row > rs || o.row > rs) return false;
+        const int64_t m = (int64_t)(o.lo - lo) % rs, shift = m < 0 ? m + rs : m;
+        return row <= shift && shift + o.row <= rs;
+    }
+    bool same(const Cover &o) const { return lo == o.lo && rs == o.rs && hs == o.hs; }
+};
 
 bool common_ok(int32_t rows, int32_t d, int32_t rot, int32_t il, int32_t dtype, float scale) {
     return rows >= 0 && d >= 1 && rot >= 0 && rot % 2 == 0 && rot <= d && (il == 0 || il == 1) &&
@@ -336,6 +357,14 @@ static gdn_status rotary(const gdn_rotary_desc *D, const uint64_t *turns, const 
         !multiple(k_out, e))
         return GDN_ERR_ALIGNMENT;
     if (D->head_dim > kRMaxRot) return GDN_ERR_UNSUPPORTED;
+    const int64_t H = D->num_heads, Hkv = D->num_kv_heads, es = e;
+    const Cover cq(q, R, D->q_row_stride, H, D->q_head_stride, d, es), ck(k, R, D->k_row_stride, Hkv, D->k_head_stride, d, es),
+        cqo(q_out, R, D->q_out_row_stride, H, D->q_out_head_stride, d, es),
+        cko(k_out, R, D->k_out_row_stride, Hkv, D->k_out_head_stride, d, es), cpos(positions, D->num_positions, 4),
+        cturns(turns, D->rot_dim / 2, 8);
+    if (!(cqo.same(cq) || cqo.apart(cq)) || !(cko.same(ck) || cko.apart(ck)) || !cqo.apart(ck) || !cko.apart(cq) ||
+        !cqo.apart(cko) || !cqo.apart(cpos) || !cko.apart(cpos) || !cqo.apart(cturns) || !cko.apart(cturns))
+        return GDN_ERR_INVALID_ARG;
     RotaryParams P = {};
     P.q = q, P.k = k, P.qo = q_out, P.ko = k_out;
     P.turns = turns, P.pos = positions;
@@ -383,6 +412,20 @@ extern "C" gdn_status gdn_rotary_append(const gdn_append_desc *D, const uint64_t
         !multiple(v, e) || !multiple(q_out, e) || !multiple(k_cache, e) || !multiple(v_cache, e) || !multiple(device_status, 4))
         return GDN_ERR_ALIGNMENT;
     if (D->head_dim > kRMaxRot) return GDN_ERR_UNSUPPORTED;
+    const int64_t Hkv = D->num_kv_heads, es = e, slots = (int64_t)D->page_size * D->num_pages;
+    const Cover cq(q, R, D->q_row_stride, D->num_heads, D->q_head_stride, d, es),
+        cqo(q_out, R, D->q_out_row_stride, D->num_heads, D->q_out_head_stride, d, es),
+        in[] = {{k, R, D->k_row_stride, Hkv, D->k_head_stride, d, es}, {v, R, D->v_row_stride, Hkv, D->v_head_stride, d, es},
+                {positions, R, 4}, {slot_map, R, 4}, {turns, D->rot_dim / 2, 8}},
+        out[] = {cqo, {k_cache, slots, Hkv * d, Hkv, d, d, es}, {v_cache, slots, Hkv * d, Hkv, d, d, es}, {device_status, 1, 4}};
+    if (!cqo.same(cq) && !cqo.apart(cq)) return GDN_ERR_INVALID_ARG;
+    for (const Cover &o : out) {
+        if (&o != out && !o.apart(cq)) return GDN_ERR_INVALID_ARG;
+        for (const Cover &i : in)
+            if (!o.apart(i)) return GDN_ERR_INVALID_ARG;
+        for (const Cover &x : out)
+            if (&x != &o && !o.apart(x)) return GDN_ERR_INVALID_ARG;
+    }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (device_status && cudaMemsetAsync(device_status, 0, sizeof(int32_t), st) != cudaSuccess) return GDN_ERR_CUDA;
     if (R == 0) return GDN_OK;

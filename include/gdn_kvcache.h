@@ -95,7 +95,10 @@ typedef struct {
 /* For every row r with slot s = slot_map[r] >= 0: q_out[r] = rotated q[r], k_cache[s] = rotated k[r],
  * v_cache[s] = v[r].  Rows with slot -1 are padding: nothing of theirs is read or written.  A slot
  * below -1 or not below p P is skipped in the same way and sets device_status (optional; cleared by the
- * call) to GDN_ERR_INVALID_ARG.  Rows that share a slot race.  q_out may be q (same strides). */
+ * call) to GDN_ERR_INVALID_ARG.  Rows that share a slot race: a slot
+ * belongs in slot_map once.  q_out may be q (same strides); every other overlap of an output (q_out, the
+ * caches, device_status) with an input or another output is GDN_ERR_INVALID_ARG, where tensors count as
+ * apart as gdn_rotary.h defines it. */
 gdn_status gdn_rotary_append(const gdn_append_desc *desc, const uint64_t *turns, const int32_t *positions,
                              const int32_t *slot_map, const void *q, const void *k, const void *v,
                              void *q_out, void *k_cache, void *v_cache, int32_t *device_status,
@@ -105,7 +108,7 @@ gdn_status gdn_rotary_append(const gdn_append_desc *desc, const uint64_t *turns,
  * num_seqs N >= 1; num_tokens L >= 1 query tokens per sequence; num_heads H, num_kv_heads H_kv
  * dividing it; head_dim d (64 or 128); page_size p; num_pages P, p P <= INT32_MAX; table_width W >= 0;
  * prefix_len Lp >= 0; causal 0 or 1; dtype GDN_BF16; scale 0 for 1/sqrt(d), else > 0 and
- * finite. */
+ * finite times log2(e). */
 typedef struct {
     int32_t num_seqs;
     int32_t num_tokens;
@@ -129,7 +132,8 @@ size_t gdn_prefix_attn_workspace_size(const gdn_prefix_attn_desc *desc);
  * sequence n, key/value head h / (H / H_kv); c = seq_lens[n] when causal = 0 (the L tokens see one
  * another), else max(0, seq_lens[n] - (L - 1 - l)) (token l is the l-th of the L newest).  A row that
  * sees no key is 0.
- *   q, out [N, L, H, d] bf16 (out must not overlap an input); workspace >= the size above, 256-byte
+ *   q, out [N, L, H, d] bf16 (neither out nor the workspace may overlap an input or one another:
+ *   GDN_ERR_INVALID_ARG); workspace >= the size above, 256-byte
  *   aligned, contents on entry ignored; its first word is the status that
  *   gdn_dual_read_device_status reads.
  * The prefix is read once for the whole batch, not once per sequence.  What lies in the cache behind

@@ -26,12 +26,14 @@
  *   positions    [T] int32 (device), R a multiple of T: row r stands at positions[r % T] (the views of
  *                the noisy stream share their positions); any int32 value is valid
  *   turns        [rot_dim / 2] uint64 (device), as gdn_rotary_frequencies wrote them
- * q_out may be q (same strides: in place), else must not overlap any input; the same for k.
+ * q_out may be q (same strides: in place), else must not overlap an input or the other output; the same
+ * for k.  Tensors whose extents overlap count as apart when they have one row stride and their rows
+ * alternate (slices of one projection's output); any other overlap is refused.
  * Arithmetic is fp32, rounded once to the dtype.
  *
  * All calls validate on the host (no partial launch on error), then enqueue on `stream` and
  * return; nothing is allocated, nothing synchronises.  Errors: GDN_ERR_INVALID_ARG (sizes, strides,
- * NULL), GDN_ERR_ALIGNMENT (positions not 4-byte, turns not 8-byte, or a tensor not aligned to its
+ * NULL, overlaps), GDN_ERR_ALIGNMENT (positions not 4-byte, turns not 8-byte, or a tensor not aligned to its
  * element), GDN_ERR_UNSUPPORTED (head_dim > 256), GDN_ERR_CUDA (launch failure).  Tensors whose
  * bases and strides are 16-byte multiples, with rot_dim a multiple of 32 bytes and head_dim of
  * 16, move in 16-byte vectors; all others take a slower path, element by element.

@@ -229,3 +229,18 @@ def test_append_far_into_a_large_cache():
     b.rotary_append(q, k, v, torch.zeros(2, dtype=torch.int32, device="cuda"), slots, table, kc, vc)
     assert torch.equal(kc.flatten(0, 1)[slots.long()], k) and torch.equal(vc.flatten(0, 1)[slots.long()], v)
     assert int(torch.count_nonzero(vc[:P // 2 - 1])) == 0 and int(torch.count_nonzero(vc[P // 2 + 2:-1])) == 0
+
+
+def test_slices_of_one_buffer_in_place_and_beside():
+    """q, k and both outputs as column slices of one buffer: their extents overlap, their rows alternate."""
+    g = _gen(21)
+    buf = _normal(g, 33, 4 + 2 + 4 + 2, 64, dtype=torch.bfloat16)
+    pos, table = torch.arange(33, dtype=torch.int32, device="cuda"), b.rotary_table(64)
+    q, k, qo, ko = buf.split((4, 2, 4, 2), dim=1)
+    want = b.rotary_forward(q.contiguous(), k.contiguous(), pos, table)
+    b.rotary_forward(q, k, pos, table, q_out=qo, k_out=ko)
+    assert torch.equal(qo, want[0]) and torch.equal(ko, want[1])
+    b.rotary_forward(q, k, pos, table, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    with pytest.raises(b.GdnError):
+        b.rotary_forward(q, k, pos, table, q_out=buf[:, 1:5], k_out=ko)

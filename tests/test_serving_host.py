@@ -96,6 +96,29 @@ def test_rotary_refuses_pointers():
     assert _call("gdn_rotary_forward", _with(ROT, num_rows=0), [None] * 6, None) == 0      # nothing to do
 
 
+# order: turns, positions, q, k, q_out, k_out
+@no_gpu
+@pytest.mark.parametrize("out,other,shift", [(4, 3, 0), (5, 2, 0), (4, 5, 0), (4, 1, -8), (5, 0, -8), (4, 2, 128), (5, 3, -2),
+                                             (4, 3, 1024)])
+def test_rotary_refuses_overlaps(out, other, shift):
+    p = list(A[:6])
+    p[out] = p[other] + shift
+    assert _call("gdn_rotary_forward", ROT, p, None) == 1
+
+
+@no_gpu
+def test_rotary_takes_an_output_behind_an_input():
+    p = list(A[:6])
+    p[4] = p[3] + 256 * 2 * 4                               # k's 6 rows of 256 bytes end 512 bytes before
+    assert _call("gdn_rotary_forward", ROT, p, None) == 4   # no device: past the checks
+
+
+@no_gpu
+def test_rotary_refuses_strides_past_any_memory():
+    for over in (dict(q_row_stride=1 << 45), dict(k_out_row_stride=1 << 62), dict(q_out_head_stride=(1 << 63) - 1)):
+        assert _call("gdn_rotary_forward", _with(ROT, **over), A[:6], None) == 1, over
+
+
 # ----------------------------------------------------------------------------- append
 APP = b.AppendDesc(6, 4, 2, 64, 64, 0, 16, 10, b.GDN_BF16, 1.0, 512, 64, 512, 64, 512, 64, 256, 64)
 
@@ -123,6 +146,16 @@ def test_append_refuses_pointers():
         assert _call("gdn_rotary_append", APP, p, None) == 2, i
     p = list(A[:10])
     p[6] = p[3]                                             # q_out = q with other strides
+    assert _call("gdn_rotary_append", APP, p, None) == 1
+
+
+# order: turns, positions, slots, q, k, v, q_out, k_cache, v_cache, status
+@no_gpu
+@pytest.mark.parametrize("out,other,shift", [(8, 7, 0), (8, 7, 16 * 10 * 2 * 64 * 2 - 2), (7, 4, 0), (8, 5, -2), (7, 3, 0),
+                                             (6, 7, 0), (6, 4, 0), (9, 2, 20), (7, 1, -2048), (6, 3, 2)])
+def test_append_refuses_overlaps(out, other, shift):
+    p = list(A[:10])
+    p[out] = p[other] + shift
     assert _call("gdn_rotary_append", APP, p, None) == 1
 
 
@@ -195,6 +228,21 @@ def test_attention_refuses_pointers():
         assert _call("gdn_prefix_attn", ATT, p, big, None) == 2, i
     size = b.prefix_attn_workspace_size(ATT)
     assert _call("gdn_prefix_attn", ATT, A[:8], ctypes.c_size_t(size - 1), None) == 1
+
+
+# order: q, k_cache, v_cache, prefix_pages, block_table, seq_lens, out, workspace
+@no_gpu
+@pytest.mark.parametrize("out,other,shift", [(6, 0, 0), (6, 1, 16), (6, 2, 100 * 16 * 2 * 128 * 2 - 16), (6, 5, 0), (7, 0, 0),
+                                             (7, 4, -256), (7, 6, 256), (6, 3, -16)])
+def test_attention_refuses_overlaps(out, other, shift):
+    p = list(A[:8])
+    p[out] = p[other] + shift
+    assert _call("gdn_prefix_attn", ATT, p, ctypes.c_size_t(1 << 60), None) == 1
+
+
+@no_gpu
+def test_attention_refuses_a_scale_past_fp32():
+    assert _call("gdn_prefix_attn", _with(ATT, scale=3e38), A[:8], ctypes.c_size_t(1 << 60), None) == 1
 
 
 # ----------------------------------------------------------------------------- the Python layer
