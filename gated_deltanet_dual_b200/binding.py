@@ -681,6 +681,13 @@ def _cuda_index(t: torch.Tensor) -> int:
     return index
 
 
+def _int32(**values):
+    """Raises when a value does not fit the descriptors' int32 (ctypes would drop its upper bits)."""
+    for name, x in values.items():
+        if not -1 << 31 <= x < 1 << 31:
+            raise ValueError(f"{name}: {x} does not fit 32 bits")
+
+
 def _fresh(shape, dtype, index: int, stream) -> torch.Tensor:
     """A new tensor for a call on `stream`.  It is allocated there: memory that the current stream has freed may still
     be written by work queued on it.  The current stream, where the caller may use it, is on its record too."""
@@ -732,6 +739,7 @@ def rotary_frequencies(rot_dim, *, base=10000.0, scaling="none", factor=1.0, ori
     """gdn_rotary_frequencies: the pairs' fractions of a turn per position, uint64 fixed point (host)."""
     if scaling not in ROPE_SCALING:
         raise ValueError(f"scaling: {scaling!r} is none of {sorted(ROPE_SCALING)}")
+    _int32(rot_dim=rot_dim)
     turns = np.zeros(max(1, int(rot_dim) // 2), dtype=np.uint64)
     st = load_library().gdn_rotary_frequencies(int(rot_dim), float(base), ROPE_SCALING[scaling], float(factor),
                                                float(original_len), float(beta_fast), float(beta_slow), turns.ctypes.data)
@@ -773,6 +781,8 @@ def _rotary(name, q, k, positions, table, q_out, k_out, stream):
                + _rows(k_out if k is not None else None, "k_out", front + (Hkv, d), io, index))
     _want(positions, "positions", (T,), torch.int32, index)
     turns = table._on(index)
+    if rows >= 1 << 31:
+        _int32(rows=rows)
     if rows and H + Hkv:
         desc = RotaryDesc(rows, T, H, Hkv, d, table._args[0], table._args[1], _dtype_code(lead), table._args[2], 0, *strides)
         _call(name, index, stream, ctypes.byref(desc), turns, positions.data_ptr(), q.data_ptr() if H else None,
@@ -834,6 +844,8 @@ def kv_extend(block_table, seq_lens, new_lens, free_pages, free_count, page_size
         raise ValueError(f"tables are made for {tables._sizes[0]} sequences on {tables.free_left.device}, not for {N} on cuda:{index}")
     if device_status is not None:
         _want(device_status, "device_status", (1,), i32, index)
+    if not (0 < page_size < 1 << 31 and 0 <= prefix_len < 1 << 31):
+        _int32(page_size=page_size, prefix_len=prefix_len)
     desc = KvExtendDesc(N, W, page_size, F, M, prefix_len, 0, 0)
     _call("gdn_kv_extend", index, stream, ctypes.byref(desc), block_table.data_ptr(), seq_lens.data_ptr(),
           new_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), *tables._ptrs,
@@ -845,7 +857,7 @@ def rotary_append(q, k, v, positions, slot_map, table: RotaryTable, k_cache, v_c
                   device_status=None, stream=None):
     """Rotary positions fused with the append to the cache (gdn_rotary_append): q [R, H, d] rotated into
     q_out, k [R, H_kv, d] rotated into k_cache [P, p, H_kv, d] and v copied into v_cache, at slot_map [R]
-    int32.  Rows with slot -1 are padding and are left as they were.  Returns q_out."""
+    int32, each slot at most once.  Rows with slot -1 are padding and are left as they were.  Returns q_out."""
     index, io = _cuda_index(q), q.dtype
     if q.ndim != 3 or k.ndim != 3 or v.ndim != 3 or k_cache.ndim != 4 or (q_out is not None and q_out.ndim != 3):
         raise ValueError("q, k, v and q_out must be [R, heads, d] and the caches [P, p, H_kv, d]")
@@ -880,6 +892,7 @@ def rotary_append(q, k, v, positions, slot_map, table: RotaryTable, k_cache, v_c
 
 def make_prefix_attn_desc(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, page_size, num_pages, table_width,
                           prefix_len, causal, scale=None, dtype_code=GDN_BF16) -> PrefixAttnDesc:
+    """gdn_prefix_attn_desc; scale None is 1 / sqrt(head_dim)."""
     return PrefixAttnDesc(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, page_size, num_pages, table_width,
                           prefix_len, 1 if causal else 0, dtype_code, 0.0 if scale is None else scale)
 
@@ -894,7 +907,9 @@ def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len, block_table,
     """Attention of the L newest tokens of N sequences, q [N, L, H, d] bf16, over a shared prefix (the
     first prefix_len tokens on the pages prefix_pages) and each sequence's own seq_lens[n] keys through
     block_table [N, W], in caches [P, p, H_kv, d] (gdn_prefix_attn).  causal=False lets the L tokens see
-    one another (a denoised block).  Returns out [N, L, H, d]."""
+    one another (a denoised block).  scale None is 1 / sqrt(d).  A workspace (Workspace, of
+    prefix_attn_workspace_size bytes) belongs to one call at a time; None allocates one.  Returns out
+    [N, L, H, d]."""
     index, io = _cuda_index(q), q.dtype
     if q.ndim != 4 or k_cache.ndim != 4 or block_table.ndim != 2:
         raise ValueError("q must be [N, L, H, d], the caches [P, p, H_kv, d] and block_table [N, W]")
@@ -912,9 +927,11 @@ def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len, block_table,
         _want(v_cache, "v_cache", (P, page, Hkv, d), io, index)
         _want(block_table, "block_table", (N, W), i32, index)
         _want(seq_lens, "seq_lens", (N,), i32, index)
-    if scale is not None and not scale > 0:
-        raise ValueError("scale must be positive")
+    if scale is not None and not ctypes.c_float(scale).value > 0:      # what fp32 makes zero would mean 1 / sqrt(d)
+        raise ValueError("scale must be positive in fp32")
     if prefix_len:
+        if prefix_pages is None:
+            raise ValueError("prefix_len needs prefix_pages")
         _want(prefix_pages, "prefix_pages", (prefix_pages.numel(),), torch.int32, index)
         if prefix_len < 0 or prefix_pages.numel() < -(-prefix_len // page):
             raise ValueError(f"prefix_pages holds {prefix_pages.numel()} pages of {page} for {prefix_len} tokens")

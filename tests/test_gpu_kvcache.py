@@ -117,3 +117,12 @@ def test_refusals():
         b.kv_extend(**ok | dict(seq_lens=t.seq_lens))       # in place
     with pytest.raises(ValueError):
         b.kv_extend(**ok | dict(block_table=_i32([[0, 1], [2, 3]])[:, :1]))
+
+
+def test_sizes_past_32_bits_are_refused():
+    def run(page, prefix):
+        return b.kv_extend(_i32([[-1, -1]]), _i32([0]), _i32([3]), _i32([7, 5]), _i32([2]), page, b.KvTables(1, 3), prefix_len=prefix)
+    assert run(16, 4).positions.tolist() == [4, 5, 6]
+    for page, prefix in (((1 << 32) + 16, 4), (16, (1 << 32) + 4), (16, -(1 << 32))):
+        with pytest.raises(ValueError):
+            run(page, prefix)

@@ -357,3 +357,39 @@ def test_buffers_of_a_call_on_another_stream():
     got_q, got_k = b.rotary_forward(q, k, pos, table, stream=side.cuda_stream)
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.equal(got_q, want_q) and torch.equal(got_k, want_k)
+
+
+def test_scales_and_pages_that_are_none():
+    p = _problem(2, 1, 4, 2, 64, 16, 40, [5, 6], seed=15)
+    for over in (dict(scale=1e-50), dict(scale=float("nan")), dict(scale=-1.0), dict(prefix_pages=None)):
+        with pytest.raises(ValueError):
+            b.prefix_attention(**dict(p, **over))
+    with pytest.raises(b.GdnError):
+        b.prefix_attention(**p, scale=3e38)
+
+
+def test_capture_behind_two_streams_and_of_an_empty_call():
+    """A capture whose call follows work joined from another stream, and one of a call without any key."""
+    p = _problem(20, 1, 8, 2, 128, 16, 700, [37] * 20, seed=16)
+    want = _run(p, True)
+    none = dict(p, prefix_len=0, block_table=p["block_table"][:, :0].contiguous(), seq_lens=_i32([0] * 20))
+    ws, side, g = b.Workspace(1 << 24), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    src, out, zero = p["q"].clone(), torch.empty_like(want), torch.empty_like(want)
+    kc, vc = p["k_cache"].clone(), p["v_cache"].clone()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        cur = torch.cuda.current_stream()
+        side.wait_stream(cur)
+        with torch.cuda.stream(side):
+            p["k_cache"].copy_(kc)
+            p["v_cache"].copy_(vc)
+        p["q"].copy_(src)
+        cur.wait_stream(side)
+        b.prefix_attention(**p, workspace=ws, out=out)
+        b.prefix_attention(**none, workspace=ws, out=zero)
+        b.prefix_attention(**p, workspace=ws, out=out)
+    for t in (p["q"], p["k_cache"], p["v_cache"], out, zero):
+        t.fill_(1.0)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and not zero.any()

@@ -260,3 +260,9 @@ def test_python_layer_wants_cuda_tensors():
         b.prefix_attention(z(1, 1, 1, 64), z(1, 16, 1, 64), z(1, 16, 1, 64), i(0), 0, i(1, 1), i(1))
     with pytest.raises(ValueError):
         b.rotary_forward(None, None, i(2), t)
+
+
+def test_python_layer_refuses_what_32_bits_do_not_hold():
+    for rot in (1 << 32, (1 << 32) + 64, -(1 << 32)):
+        with pytest.raises(ValueError):
+            b.rotary_frequencies(rot)
