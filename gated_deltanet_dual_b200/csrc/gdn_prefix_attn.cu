@@ -1122,16 +1122,25 @@ struct Plan {
 // SMs, and each part a little in the combine step.  With own keys beside it a prefix is thus cut into fewer
 // parts than would fill the GPU: 16384 keys for 256 requests of up to 1024 own tokens, 3 parts of 32 CTAs
 // 110 us, 4 parts 123 us (2 parts 132 us); the prefix alone, 92 us and 75 us.
+// The host knows the tables' room, not the lengths, so the prefix's own time may grow by kMost at the most: 64 requests of
+// up to 1024 own tokens over 8192 prefix keys take 48 us with tables of that room and 50 us with 128 times it (150 us
+// without the limit); a limit of 1.35 costs the former 3 us and gains the latter nothing.
 int tile_split(int64_t base, int64_t tiles, double beside) {
-    constexpr double kTileUs = 1.6, kStartUs = 12.0, kPartUs = 0.3;
+    constexpr double kTileUs = 1.6, kStartUs = 12.0, kPartUs = 0.3, kMost = 1.65;
     int best = 1;
-    double cost = 1e300;
-    for (int s = 1; s <= kMaxSplits && s <= tiles; ++s) {
-        const double cta = (double)((tiles + s - 1) / s) * kTileUs + kStartUs;
-        const double waves = (double)((base * s + kSms - 1) / kSms) * cta;
-        const double c = std::max(waves, ((double)(base * s) * cta + beside) / kSms) + kPartUs * s;
-        if (c < cost * 0.999) cost = c, best = s;
-    }
+    double least = 1e300, cost = 1e300;
+    for (int pass = 0; pass < 2; ++pass)
+        for (int s = 1; s <= kMaxSplits && s <= tiles; ++s) {
+            const double cta = (double)((tiles + s - 1) / s) * kTileUs + kStartUs;
+            const double waves = (double)((base * s + kSms - 1) / kSms) * cta;
+            if (pass == 0) {
+                least = std::min(least, waves);
+                continue;
+            }
+            if (waves > kMost * least) continue;
+            const double c = std::max(waves, ((double)(base * s) * cta + beside) / kSms) + kPartUs * s;
+            if (c < cost * 0.999) cost = c, best = s;
+        }
     return best;
 }
 
