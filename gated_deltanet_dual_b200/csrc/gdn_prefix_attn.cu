@@ -913,7 +913,11 @@ gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
                 if (lane < 4) s_ml[warp][n * 8 + 2 * lane + e] = make_float2(m_ref[n][e], l);
             }
     }
-    __syncthreads();                           // the ring is free: the warps' O^T go there, [warp][row][d]
+    // The ring is free: the warps' O^T go there, [warp][row][d], with 4 floats behind a row (a warp's writes to its 4
+    // rows x 8 columns then meet no bank twice)
+    constexpr int kRow = D + 4;
+    static_assert(4 * NT * 8 * kRow * 4 <= kWStages * 2 * kTileBytes, "the warps' O must fit the ring");
+    __syncthreads();
     float *so = reinterpret_cast<float *>(sm);
     if (warp < 4) {
 #pragma unroll
@@ -927,7 +931,7 @@ gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
                 // a warp without a visible key has m = -inf and adds nothing (0 x anything is dropped)
                 const bool none = m_ref[n][e] == -INFINITY;
                 const float f = none ? 0.f : ex2_approx(m_ref[n][e] - m);
-                float *dst = so + (warp * (NT * 8) + row) * D + (lane >> 2);
+                float *dst = so + (warp * (NT * 8) + row) * kRow + (lane >> 2);
 #pragma unroll
                 for (int d0 = 0; d0 < D / 16; ++d0) {
                     dst[d0 * 16] = none ? 0.f : acc[d0][n][e] * f;
@@ -948,7 +952,7 @@ gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-            const float4 u = reinterpret_cast<const float4 *>(so)[(y * (NT * 8) + row) * (D / 4) + c];
+            const float4 u = reinterpret_cast<const float4 *>(so)[(y * (NT * 8) + row) * (kRow / 4) + c];
             o.x += u.x, o.y += u.y, o.z += u.z, o.w += u.w;
         }
         reinterpret_cast<float4 *>(P.part_o + (w.part * P.rows + row_of(P, w.hk, w.row0 + row)) * D)[c] = o;
@@ -974,9 +978,9 @@ __global__ void __launch_bounds__(128) gdn_attn_combine_kernel(const __grid_cons
     const int64_t row = ((int64_t)blockIdx.x * 128 + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
     const int h = (int)(row % P.H), l = (int)(row / P.H % P.L), n = (int)(row / P.H / P.L);
+    const int s = row < P.rows ? own_len(P, n) : 0;       // an input: on its way beside the wait
     grid_wait();
     if (row >= P.rows) return;
-    const int s = own_len(P, n);
     float m = -INFINITY, sum = 0.f, acc[C];
     int status = s < 0 ? (int)GDN_ERR_INVALID_ARG : 0;
 #pragma unroll
@@ -1148,7 +1152,7 @@ int tile_split(int64_t base, int64_t tiles, double beside) {
 // three CTAs for each place on the GPU while no split gets shorter than its least.
 int warp_split(int64_t base, int64_t keys) {
     const int64_t most = (keys + kWKeys * kWMinTiles - 1) / (kWKeys * kWMinTiles);
-    return (int)std::max<int64_t>(1, std::min<int64_t>({(8 * kSms + base - 1) / base, most, kMaxSplits}));
+    return (int)std::max<int64_t>(1, std::min<int64_t>({(6 * kSms + base - 1) / base, most, kMaxSplits}));
 }
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
