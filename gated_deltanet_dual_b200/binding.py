@@ -660,13 +660,15 @@ def _rows(t: Optional[torch.Tensor], name: str, shape, dtype, index: int):
     """(row stride, head stride) in elements of [..., rows, heads, d] with contiguous heads."""
     if t is None:
         return 0, 0
+    st = t.stride()
+    if t.shape == shape and t.dtype is dtype and st[-1] == 1 and len(st) == 3 and t.get_device() == index:
+        return st[0], st[1]
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype} != {dtype}")
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-    st = t.stride()
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
     if len(shape) == 4 and shape[0] > 1 and st[0] != shape[1] * st[1]:
@@ -688,14 +690,15 @@ def _int32(**values):
             raise ValueError(f"{name}: {x} does not fit 32 bits")
 
 
-def _fresh(shape, dtype, index: int, stream) -> torch.Tensor:
+def _fresh(like: torch.Tensor, shape, stream, dtype=None) -> torch.Tensor:
     """A new tensor for a call on `stream`.  It is allocated there: memory that the current stream has freed may still
     be written by work queued on it.  The current stream, where the caller may use it, is on its record too."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+        return like.new_empty(shape, dtype=dtype)
+    index = like.get_device()
     current = torch.cuda.current_stream(index)
     with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=index)):
-        t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+        t = like.new_empty(shape, dtype=dtype)
     if stream != current.cuda_stream:
         t.record_stream(current)
     return t
@@ -764,21 +767,27 @@ def _rotary(name, q, k, positions, table, q_out, k_out, stream):
     lead = q if q is not None else k
     if lead is None:
         raise ValueError("q and k are both None")
-    index, io = _cuda_index(lead), lead.dtype
-    if lead.ndim not in (3, 4):
+    index, io, shape = _cuda_index(lead), lead.dtype, lead.shape
+    if len(shape) not in (3, 4):
         raise ValueError("q and k must be [T, H, d] or [V, T, H, d]")
-    front, d = lead.shape[:-2], lead.shape[-1]
+    front, d = shape[:-2], shape[-1]
     T = front[-1]
+    rows = T if len(front) == 1 else T * front[0]
     H = q.shape[-2] if q is not None else 0
     Hkv = k.shape[-2] if k is not None else 0
-    rows = T * (front[0] if len(front) == 2 else 1)
+    q_shape, k_shape = front + (H, d), front + (Hkv, d)
+    strides = _rows(q, "q", q_shape, io, index) + _rows(k, "k", k_shape, io, index)
+    for given, out, label, want in ((q, q_out, "q_out", q_shape), (k, k_out, "k_out", k_shape)):
+        if given is None:
+            strides += 0, 0
+        elif out is None:
+            strides += want[-2] * d, d         # of a new tensor
+        else:
+            strides += _rows(out, label, want, io, index)
     if q is not None and q_out is None:
-        q_out = _fresh(front + (H, d), io, index, stream)
+        q_out = _fresh(q, q_shape, stream)
     if k is not None and k_out is None:
-        k_out = _fresh(front + (Hkv, d), io, index, stream)
-    strides = (_rows(q, "q", front + (H, d), io, index) + _rows(k, "k", front + (Hkv, d), io, index)
-               + _rows(q_out if q is not None else None, "q_out", front + (H, d), io, index)
-               + _rows(k_out if k is not None else None, "k_out", front + (Hkv, d), io, index))
+        k_out = _fresh(k, k_shape, stream)
     _want(positions, "positions", (T,), torch.int32, index)
     turns = table._on(index)
     if rows >= 1 << 31:
@@ -864,7 +873,7 @@ def rotary_append(q, k, v, positions, slot_map, table: RotaryTable, k_cache, v_c
     R, H, d = q.shape
     Hkv, (P, page) = k.shape[1], k_cache.shape[:2]
     if q_out is None:
-        q_out = _fresh((R, H, d), io, index, stream)
+        q_out = _fresh(q, (R, H, d), stream)
     (qr, qh, q1), (kr, kh, k1), (vr, vh, v1), (outr, outh, out1) = q.stride(), k.stride(), v.stride(), q_out.stride()
     if not (q1 == k1 == v1 == out1 == 1 and k.shape[0] == R and k.shape[2] == d and v.shape == k.shape
             and q_out.shape == q.shape and k_cache.shape == v_cache.shape == (P, page, Hkv, d) and k.dtype is io
@@ -936,13 +945,13 @@ def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len, block_table,
         if prefix_len < 0 or prefix_pages.numel() < -(-prefix_len // page):
             raise ValueError(f"prefix_pages holds {prefix_pages.numel()} pages of {page} for {prefix_len} tokens")
     if out is None:
-        out = _fresh(shape, io, index, stream)
+        out = _fresh(q, shape, stream)
     else:
         _want(out, "out", shape, io, index)
     desc = PrefixAttnDesc(N, L, H, Hkv, d, page, P, W, prefix_len, 1 if causal else 0, _dtype_code(q),
                           0.0 if scale is None else scale)
     if workspace is None:
-        ws = _fresh((max(256, prefix_attn_workspace_size(desc)),), torch.uint8, index, stream)
+        ws = _fresh(q, (max(256, prefix_attn_workspace_size(desc)),), stream, torch.uint8)
     else:
         ws = workspace.tensor
         if ws.get_device() != index:
