@@ -17,7 +17,7 @@
 // when it moves.  S_A and S_B take turns in the same TMEM columns, which are free as soon as the scores are in
 // registers; P (bf16) has columns of its own per row tile, so S(next) runs while this tile's exponentials
 // do.  Bound by the exponential unit and the shared memory reads of the products together: 256 requests of 4
-// query heads per key/value head over 16384 prefix keys take 75 us where the products alone are 40 us of the tensor
+// query heads per key/value head over 16384 prefix keys take 74 us where the products alone are 40 us of the tensor
 // pipe's measured rate and the exponentials 30 us.
 //
 // gdn_warp_attn_kernel -- few query rows of a key list (L (H / H_kv) <= 16: a decode step): bound by
@@ -25,9 +25,15 @@
 // with its own pages loaded by TMA into a ring of 64-key tiles.  Each of four warps takes 16 keys of
 // every tile with a softmax state of its own, so warps never wait for one another inside the loop:
 // S^T = K Q^T (mma m16n8k16, keys x rows, so 8 rows cost one column tile), P^T transposed in
-// registers (movmatrix) into the B operand of O^T += V^T P^T.  The warps' states are joined at the end.
+// registers (movmatrix) into the B operand of O^T += V^T P^T.  The warps' states are joined at the end.  32
+// requests of up to 16384 own tokens, 32 query heads on 8: 184 us, the time of one read at 6.46 TB/s; of short
+// lists the start and end show: 64 requests of up to 1024 tokens 33 us, where one read takes 21.
 //
-// gdn_attn_combine_kernel -- one warp per row joins the parts and rounds once to bf16.
+// P is rounded to bf16 for the second product: each term of a row's sum is off by at most 2^-8 of itself, in the
+// size of the output's own rounding; its sum l is taken before the rounding, in fp32, as is everything else.
+//
+// gdn_attn_combine_kernel -- one warp per row joins the parts and rounds once to bf16.  Bound by latency (the wait
+// for the parts, then two dependent reads from L2): about 4 us of a call.
 //
 // A sequence's last tile holds rows behind its last token, which may be anything: their scores are
 // masked and their V rows are set to zero in shared memory (0 x NaN would be NaN in the MMA).  Among the
@@ -673,9 +679,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Tiles on their way: at d = 128 three CTAs an SM of two tiles (64 KB each, 136 registers a thread) beat two CTAs of
+// Tiles on their way: at d = 128 three CTAs an SM of two tiles (64 KB each, at most 136 registers a thread) beat two CTAs of
 // three, because one CTA's start lies behind two others' loads (own keys of 64 requests of up to 1024
-// tokens, 32 query heads on 8: 35 against 40 us; of 32 requests with 4 tokens each, 47 against 61 us).
+// tokens, 32 query heads on 8, 35 against 40 us; of 32 requests with 4 tokens each, 47 against 61 us, both with
+// the splits of that time; with the present ones 33 and 41 us).  One set of CTAs that stay and take one item after the
+// other without a gap in the loads was slower (37 and 55 us): the gaps of one CTA lie behind the others anyway.
 template <int D, int NT>
 constexpr int warp_stages() { return D == 128 ? 2 : 3; }
 template <int D, int NT>
@@ -1125,9 +1133,9 @@ struct Plan {
 // end (measured at two row tiles, d = 128); the call takes as long as its waves of CTAs, or as all its work on all
 // SMs, and each part a little in the combine step.  With own keys beside it a prefix is thus cut into fewer
 // parts than would fill the GPU: 16384 keys for 256 requests of up to 1024 own tokens, 3 parts of 32 CTAs
-// 110 us, 4 parts 123 us (2 parts 132 us); the prefix alone, 92 us and 75 us.
+// 107 us, 4 parts 120 us (2 parts 130 us); the prefix alone, 92 us and 74 us.
 // The host knows the tables' room, not the lengths, so the prefix's own time may grow by kMost at the most: 64 requests of
-// up to 1024 own tokens over 8192 prefix keys take 48 us with tables of that room and 50 us with 128 times it (150 us
+// up to 1024 own tokens over 8192 prefix keys take 45 us with tables of that room and 45 us with 32 times it (150 us
 // without the limit); a limit of 1.35 costs the former 3 us and gains the latter nothing.
 int tile_split(int64_t base, int64_t tiles, double beside) {
     constexpr double kTileUs = 1.6, kStartUs = 12.0, kPartUs = 0.3, kMost = 1.65;
@@ -1148,8 +1156,11 @@ int tile_split(int64_t base, int64_t tiles, double beside) {
     return best;
 }
 
-// The same for gdn_warp_attn_kernel, whose CTAs share an SM and whose lists differ in length: about
-// three CTAs for each place on the GPU while no split gets shorter than its least.
+// The same for gdn_warp_attn_kernel, whose CTAs share an SM and whose lists differ in length: about two CTAs for
+// each of its places on the GPU while no split gets shorter than its least.  A part costs its rows of O a write and a
+// read: 64 requests of up to 1024 own tokens over 8192 prefix keys take 45.7 us with 6 CTAs a SM (2 parts) and 48.9 with
+// 8 (3 parts), 32 blocks of 4 over 32768 104 and 110 us; with 4 CTAs a SM, 32 requests of up to 16384 own
+// tokens wait for the longest (194 against 187 us).
 int warp_split(int64_t base, int64_t keys) {
     const int64_t most = (keys + kWKeys * kWMinTiles - 1) / (kWKeys * kWMinTiles);
     return (int)std::max<int64_t>(1, std::min<int64_t>({(6 * kSms + base - 1) / base, most, kMaxSplits}));

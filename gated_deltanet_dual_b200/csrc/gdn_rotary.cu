@@ -10,7 +10,10 @@
 // first compute the rows' (cos, sin) once for all heads into shared memory, then each thread keeps
 // one column unit (two 16-byte vectors whose elements pair up, or one vector of interleaved
 // pairs) and walks over (row, head), a few heads at a time, holding its unit's cos and sin in registers
-// within a row.
+// within a row.  8 x 4096 rows of 16 + 16 heads of 128 in bf16 take 88.6 us (6.06 TB/s; one read and write at the
+// copy rate of 6.46 takes 83.2), gradients of two fp32 views with half of each head in pairs 84 us (78.0), the
+// append of 8192 rows 36.0 us (30.9).  More heads at a time cost registers and so CTAs (four in the half
+// layout: 126 us).
 #include <algorithm>
 #include <cmath>
 
