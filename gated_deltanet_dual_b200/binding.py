@@ -30,7 +30,7 @@ EXPORTED = ("gdn_dual_forward", "gdn_dual_workspace_size", "gdn_dual_read_device
             "gdn_dual_backward_conv", "gdn_dual_backward_conv_workspace_size",
             "gdn_dual_forward_host", "gdn_dual_host_staging_size", "gdn_dual_host_read_device_status",
             "gdn_rotary_frequencies", "gdn_rotary_forward", "gdn_rotary_backward", "gdn_rotary_append",
-            "gdn_kv_extend", "gdn_prefix_attn", "gdn_prefix_attn_workspace_size")
+            "gdn_kv_extend", "gdn_prefix_attn", "gdn_prefix_attn_workspace_size", "gdn_prefix_attn_test_wait_limit")
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "ramp": 3}
 
 
@@ -960,3 +960,16 @@ def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len, block_table,
           prefix_pages.data_ptr() if prefix_len else None, block_table.data_ptr() if W else None, seq_lens.data_ptr(),
           out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
+
+
+def prefix_attention_test_wait_limit_raw(desc: PrefixAttnDesc, q, k_cache, v_cache, prefix_pages, block_table, seq_lens,
+                                         out, workspace, wait_iters: int, stream=None) -> int:
+    """C-ABI call of gdn_prefix_attn_test_wait_limit (tests of the bounded-wait error path only).
+    Returns the status code."""
+    fn = load_library().gdn_prefix_attn_test_wait_limit
+    vp = ctypes.c_void_p
+    fn.restype = ctypes.c_int
+    fn.argtypes = [ctypes.POINTER(PrefixAttnDesc)] + [vp] * 8 + [ctypes.c_size_t, ctypes.c_uint32, vp]
+    return int(fn(ctypes.byref(desc), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_pages), _ptr(block_table),
+                  _ptr(seq_lens), _ptr(out), _ptr(workspace), ctypes.c_size_t(workspace.numel()),
+                  ctypes.c_uint32(wait_iters), _stream(stream)))

@@ -91,6 +91,7 @@ struct PrefixParams {
     int32_t prefix_tiles, prefix_splits, own_tiles, own_splits;   // *_tiles: CTAs over the rows
     int32_t prefix_rows, own_rows;             // rows of such a CTA
     float scale_log2;
+    uint32_t wait_iters;                       // polls of a wait in the test instantiations
 };
 
 __device__ __forceinline__ float ex2_approx(float x) {
@@ -269,7 +270,8 @@ struct PrefixMaps {
     CUtensorMap k, v;                          // [P p, H_kv, d], box: 64 columns x 1 head x min(p, 64) rows
 };
 
-template <int D>
+// TW: the test instantiation, whose waits poll with the caller's bound (gdn_prefix_attn_test_wait_limit).
+template <int D, bool TW>
 __global__ void __launch_bounds__(kTThreads, 1)
 gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ PrefixMaps M) {
     constexpr int kHalves = D / 64;
@@ -386,10 +388,14 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
     // their pairs, run through their tiles (on unspecified data) and write nothing.
     auto stopped = [&] { return *reinterpret_cast<volatile int *>(&s_abort) != 0; };
     auto wait = [&](uint64_t *bar, uint32_t parity, int where) {
-        if (mbar_try_wait(bar, parity)) return;
-        for (uint32_t it = 0; it < kPWaitIters / 16; ++it) {
-            if (mbar_wait_some(bar, parity)) return;
-            if (stopped()) return;
+        if constexpr (TW) {
+            if (stopped() || mbar_poll(bar, parity, P.wait_iters)) return;
+        } else {
+            if (mbar_try_wait(bar, parity)) return;
+            for (uint32_t it = 0; it < kPWaitIters / 16; ++it) {
+                if (mbar_wait_some(bar, parity)) return;
+                if (stopped()) return;
+            }
         }
         if (atomicExch(&s_abort, 1) == 0) atomicExch(&s_status, (int)GDN_ERR_TIMEOUT | where << 16);
     };
@@ -689,8 +695,8 @@ constexpr int warp_stages() { return D == 128 ? 2 : 3; }
 template <int D, int NT>
 constexpr int warp_smem() { return warp_stages<D, NT>() * 2 * kWKeys * D * 2 + 1024; }
 
-// NT: column tiles of 8 rows.
-template <int D, int NT>
+// NT: column tiles of 8 rows.  TW: as above.
+template <int D, int NT, bool TW>
 __global__ void __maxnreg__(136)
 gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ PrefixMaps M) {
     constexpr int kHalves = D / 64;
@@ -731,10 +737,14 @@ gdn_warp_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
     // stop, the other warps run through their tiles (on unspecified data).
     auto stopped = [&] { return *reinterpret_cast<volatile int *>(&s_abort) != 0; };
     auto wait = [&](uint64_t *bar, uint32_t parity, int where) {
-        if (mbar_try_wait(bar, parity)) return;
-        for (uint32_t it = 0; it < kPWaitIters / 16; ++it) {
-            if (mbar_wait_some(bar, parity)) return;
-            if (stopped()) return;
+        if constexpr (TW) {
+            if (stopped() || mbar_poll(bar, parity, P.wait_iters)) return;
+        } else {
+            if (mbar_try_wait(bar, parity)) return;
+            for (uint32_t it = 0; it < kPWaitIters / 16; ++it) {
+                if (mbar_wait_some(bar, parity)) return;
+                if (stopped()) return;
+            }
         }
         if (atomicExch(&s_abort, 1) == 0) atomicOr(&s_status, (int)GDN_ERR_TIMEOUT | where << 16);
     };
@@ -1198,7 +1208,7 @@ template <int D>
 constexpr int tile_smem() { return (2 + kStages) * kTile * D * 2 + 1024; }
 
 // Raises the kernels' dynamic shared memory limits, once per device.
-template <int D>
+template <int D, bool TW>
 cudaError_t prepare_device() {
     static std::atomic<uint64_t> done{0};
     int dev = 0;
@@ -1207,13 +1217,13 @@ cudaError_t prepare_device() {
     const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
     if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
     constexpr auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    e = cudaFuncSetAttribute(gdn_tile_attn_kernel<D>, attr, tile_smem<D>());
+    e = cudaFuncSetAttribute(gdn_tile_attn_kernel<D, TW>, attr, tile_smem<D>());
     // the shares that its warps take add up to what it is launched with, or they would wait for ever
     cudaFuncAttributes fa;
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, gdn_tile_attn_kernel<D>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, gdn_tile_attn_kernel<D, TW>);
     if (e == cudaSuccess && fa.numRegs < kRegsLaunch) e = cudaErrorInvalidConfiguration;
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_warp_attn_kernel<D, 1>, attr, warp_smem<D, 1>());
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_warp_attn_kernel<D, 2>, attr, warp_smem<D, 2>());
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_warp_attn_kernel<D, 1, TW>, attr, warp_smem<D, 1>());
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_warp_attn_kernel<D, 2, TW>, attr, warp_smem<D, 2>());
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
     return e;
 }
@@ -1232,27 +1242,27 @@ cudaError_t launch_dependent(void (*kernel)(KArgs...), unsigned grid, unsigned t
 }
 
 // One launch over items [first, first + count).
-template <int D>
+template <int D, bool TW>
 cudaError_t launch_parts(PrefixParams P, const PrefixMaps &maps, bool warp, int64_t rows, int64_t first, int64_t count,
                          cudaStream_t st) {
     if (count == 0) return cudaSuccess;
     P.first_item = (int32_t)first;
-    if (!warp) return launch_dependent(gdn_tile_attn_kernel<D>, (unsigned)count, kTThreads, tile_smem<D>(), st, P, maps);
-    if (rows <= 8) return launch_dependent(gdn_warp_attn_kernel<D, 1>, (unsigned)count, kWThreads, warp_smem<D, 1>(), st, P, maps);
-    return launch_dependent(gdn_warp_attn_kernel<D, 2>, (unsigned)count, kWThreads, warp_smem<D, 2>(), st, P, maps);
+    if (!warp) return launch_dependent(gdn_tile_attn_kernel<D, TW>, (unsigned)count, kTThreads, tile_smem<D>(), st, P, maps);
+    if (rows <= 8) return launch_dependent(gdn_warp_attn_kernel<D, 1, TW>, (unsigned)count, kWThreads, warp_smem<D, 1>(), st, P, maps);
+    return launch_dependent(gdn_warp_attn_kernel<D, 2, TW>, (unsigned)count, kWThreads, warp_smem<D, 2>(), st, P, maps);
 }
 
-template <int D>
+template <int D, bool TW>
 gdn_status launch(const PrefixParams &P, const PrefixMaps &maps, const Plan &plan, cudaStream_t st) {
-    if (prepare_device<D>() != cudaSuccess) return GDN_ERR_CUDA;
+    if (prepare_device<D, TW>() != cudaSuccess) return GDN_ERR_CUDA;
     const int64_t own_rows = (int64_t)P.L * P.G, all_rows = P.N * own_rows;
     const bool both = plan.prefix_warp == plan.own_warp && plan.own_items > 0;
     cudaError_t e = cudaSuccess;
     if (plan.prefix_items + plan.own_items == 0) e = cudaMemsetAsync(P.ws, 0, sizeof(WorkspaceHeader), st);
     if (e == cudaSuccess)
-        e = launch_parts<D>(P, maps, plan.prefix_warp, plan.prefix_items ? all_rows : own_rows, 0,
+        e = launch_parts<D, TW>(P, maps, plan.prefix_warp, plan.prefix_items ? all_rows : own_rows, 0,
                             plan.prefix_items + (both ? plan.own_items : 0), st);
-    if (e == cudaSuccess && !both) e = launch_parts<D>(P, maps, plan.own_warp, own_rows, plan.prefix_items, plan.own_items, st);
+    if (e == cudaSuccess && !both) e = launch_parts<D, TW>(P, maps, plan.own_warp, own_rows, plan.prefix_items, plan.own_items, st);
     if (e == cudaSuccess)
         e = launch_dependent(gdn_attn_combine_kernel<D>, (unsigned)((plan.rows + 3) / 4), 128, 0, st, P, plan.parts);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
@@ -1268,10 +1278,10 @@ extern "C" size_t gdn_prefix_attn_workspace_size(const gdn_prefix_attn_desc *des
     return plan_of(desc).bytes;
 }
 
-extern "C" gdn_status gdn_prefix_attn(const gdn_prefix_attn_desc *D, const void *q, const void *k_cache,
-                                      const void *v_cache, const int32_t *prefix_pages, const int32_t *block_table,
-                                      const int32_t *seq_lens, void *out, void *workspace, size_t workspace_bytes,
-                                      gdn_stream_t stream) {
+// wait_iters 0: the normal bound.
+static gdn_status prefix_attn(const gdn_prefix_attn_desc *D, const void *q, const void *k_cache, const void *v_cache,
+                              const int32_t *prefix_pages, const int32_t *block_table, const int32_t *seq_lens, void *out,
+                              void *workspace, size_t workspace_bytes, uint32_t wait_iters, gdn_stream_t stream) {
     if (!desc_ok(D)) return GDN_ERR_INVALID_ARG;
     if (!q || !k_cache || !v_cache || !seq_lens || !out || !workspace || (D->prefix_len > 0 && !prefix_pages) ||
         (D->table_width > 0 && !block_table))
@@ -1320,5 +1330,25 @@ extern "C" gdn_status gdn_prefix_attn(const gdn_prefix_attn_desc *D, const void 
     PrefixMaps maps;
     if (!cache_map(&maps.k, k_cache, D) || !cache_map(&maps.v, v_cache, D)) return GDN_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return D->head_dim == 64 ? launch<64>(P, maps, plan, st) : launch<128>(P, maps, plan, st);
+    P.wait_iters = wait_iters;
+    if (wait_iters) return D->head_dim == 64 ? launch<64, true>(P, maps, plan, st) : launch<128, true>(P, maps, plan, st);
+    return D->head_dim == 64 ? launch<64, false>(P, maps, plan, st) : launch<128, false>(P, maps, plan, st);
+}
+
+extern "C" gdn_status gdn_prefix_attn(const gdn_prefix_attn_desc *desc, const void *q, const void *k_cache,
+                                      const void *v_cache, const int32_t *prefix_pages, const int32_t *block_table,
+                                      const int32_t *seq_lens, void *out, void *workspace, size_t workspace_bytes,
+                                      gdn_stream_t stream) {
+    return prefix_attn(desc, q, k_cache, v_cache, prefix_pages, block_table, seq_lens, out, workspace, workspace_bytes, 0,
+                       stream);
+}
+
+extern "C" gdn_status gdn_prefix_attn_test_wait_limit(const gdn_prefix_attn_desc *desc, const void *q, const void *k_cache,
+                                                      const void *v_cache, const int32_t *prefix_pages,
+                                                      const int32_t *block_table, const int32_t *seq_lens, void *out,
+                                                      void *workspace, size_t workspace_bytes, uint32_t wait_iters,
+                                                      gdn_stream_t stream) {
+    if (wait_iters == 0) return GDN_ERR_INVALID_ARG;
+    return prefix_attn(desc, q, k_cache, v_cache, prefix_pages, block_table, seq_lens, out, workspace, workspace_bytes,
+                       wait_iters, stream);
 }

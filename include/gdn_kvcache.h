@@ -148,6 +148,16 @@ gdn_status gdn_prefix_attn(const gdn_prefix_attn_desc *desc, const void *q, cons
                            const int32_t *seq_lens, void *out, void *workspace, size_t workspace_bytes,
                            gdn_stream_t stream);
 
+/* FOR TESTS of the bounded-wait error path only: gdn_prefix_attn with every device-side wait bounded by
+ * `wait_iters` non-blocking polls (>= 1).  A wait that gives up records GDN_ERR_TIMEOUT in the
+ * workspace; the kernels then wait with the normal bound for every copy and MMA they issued before
+ * they leave; the output is unspecified. */
+gdn_status gdn_prefix_attn_test_wait_limit(const gdn_prefix_attn_desc *desc, const void *q, const void *k_cache,
+                                           const void *v_cache, const int32_t *prefix_pages,
+                                           const int32_t *block_table, const int32_t *seq_lens, void *out,
+                                           void *workspace, size_t workspace_bytes, uint32_t wait_iters,
+                                           gdn_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -393,3 +393,36 @@ def test_capture_behind_two_streams_and_of_an_empty_call():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want) and not zero.any()
+
+
+@pytest.mark.parametrize("N,L,H,Hkv,d,prefix,own", [(20, 2, 8, 2, 128, 900, 37), (2, 1, 4, 2, 64, 700, 300), (3, 40, 4, 4, 64, 700, 300),
+                                                    (2, 40, 4, 2, 128, 0, 900), (9, 8, 8, 4, 128, 0, 900)])
+def test_wait_gives_up_then_next_call_is_correct(N, L, H, Hkv, d, prefix, own):
+    p = _problem(N, L, H, Hkv, d, 16, prefix, [own] * N, seed=17)
+    ws, out = b.Workspace(1 << 25), torch.empty_like(p["q"])
+    want = _run(p, True)
+    desc = b.make_prefix_attn_desc(N, L, H, Hkv, d, 16, p["k_cache"].shape[0], p["block_table"].shape[1], prefix, True)
+    for attempt in range(2):
+        st = b.prefix_attention_test_wait_limit_raw(desc, p["q"], p["k_cache"], p["v_cache"], p["prefix_pages"],
+                                                    p["block_table"], p["seq_lens"], out, ws.tensor, 1)
+        assert st == b.GDN_OK, b.status_string(st)
+        status, where = b.read_device_status_where(ws.tensor)
+        assert status == b.GDN_ERR_TIMEOUT and where > 0, (attempt, status, where)
+    assert torch.equal(b.prefix_attention(**p, workspace=ws), want)
+    assert b.read_device_status_where(ws.tensor) == (b.GDN_OK, 0)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams with a workspace each run beside one another and give the bits that they give alone."""
+    ps = [_problem(20, 2, 8, 2, 128, 16, 900, [37] * 20, seed=18), _problem(16, 1, 8, 2, 64, 32, 1500, [200] * 16, seed=19)]
+    want = [_run(p, True) for p in ps]
+    streams, ws = [torch.cuda.Stream() for _ in ps], [b.Workspace(1 << 25) for _ in ps]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(100):
+        for p, s, w, o in zip(ps, streams, ws, outs):
+            with torch.cuda.stream(s):
+                o.append(b.prefix_attention(**p, workspace=w))
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert all(torch.equal(x, w) for x in o)

@@ -266,3 +266,8 @@ def test_python_layer_refuses_what_32_bits_do_not_hold():
     for rot in (1 << 32, (1 << 32) + 64, -(1 << 32)):
         with pytest.raises(ValueError):
             b.rotary_frequencies(rot)
+
+
+@no_gpu
+def test_wait_limit_of_zero_is_refused():
+    assert _call("gdn_prefix_attn_test_wait_limit", ATT, A[:8], ctypes.c_size_t(1 << 60), ctypes.c_uint32(0), None) == 1
