@@ -426,3 +426,10 @@ def test_two_calls_at_once():
     torch.cuda.synchronize()
     for o, w in zip(outs, want):
         assert all(torch.equal(x, w) for x in o)
+
+
+@pytest.mark.parametrize("N,L,H,Hkv,d,page", [(40, 1, 16, 2, 128, 16), (3, 4, 4, 1, 64, 64)])
+def test_tables_far_wider_than_the_lengths(N, L, H, Hkv, d, page):
+    lens = np.random.default_rng(N).integers(0, 90, N).tolist()
+    p = _problem(N, L, H, Hkv, d, page, 3000, lens, W=4000, seed=20)
+    _close(_run(p, True), _oracle(p, True), d)
