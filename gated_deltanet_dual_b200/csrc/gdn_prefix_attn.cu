@@ -1143,12 +1143,12 @@ struct Plan {
 // end (measured at two row tiles, d = 128); the call takes as long as its waves of CTAs, or as all its work on all
 // SMs, and each part a little in the combine step.  With own keys beside it a prefix is thus cut into fewer
 // parts than would fill the GPU: 16384 keys for 256 requests of up to 1024 own tokens, 3 parts of 32 CTAs
-// 107 us, 4 parts 120 us (2 parts 130 us); the prefix alone, 92 us and 74 us.
-// The host knows the tables' room, not the lengths, so the prefix's own time may grow by kMost at the most: 64 requests of
-// up to 1024 own tokens over 8192 prefix keys take 45 us with tables of that room and 45 us with 32 times it (150 us
-// without the limit); a limit of 1.35 costs the former 3 us and gains the latter nothing.
+// 108 us, 4 parts 122 us (2 parts 131 us); the prefix alone, 92 us and 74 us.
+// The host knows the tables' room, not the lengths, so the prefix's own time may grow by a third and 6.5 us at the most: 64
+// requests of up to 1024 own tokens over 8192 prefix keys take 45 us with tables of that room (6 parts; 5 parts 48 us,
+// 8 parts 50) and with 32 times it (150 us without the limit); 24 x 8 drafts at d = 64 over 1001 keys 41 us (1 part; 2 parts 44).
 int tile_split(int64_t base, int64_t tiles, double beside) {
-    constexpr double kTileUs = 1.6, kStartUs = 12.0, kPartUs = 0.3, kMost = 1.65;
+    constexpr double kTileUs = 1.6, kStartUs = 12.0, kPartUs = 0.3, kMost = 1.35, kMostUs = 6.5;
     int best = 1;
     double least = 1e300, cost = 1e300;
     for (int pass = 0; pass < 2; ++pass)
@@ -1159,7 +1159,7 @@ int tile_split(int64_t base, int64_t tiles, double beside) {
                 least = std::min(least, waves);
                 continue;
             }
-            if (waves > kMost * least) continue;
+            if (waves > kMost * least + kMostUs) continue;
             const double c = std::max(waves, ((double)(base * s) * cta + beside) / kSms) + kPartUs * s;
             if (c < cost * 0.999) cost = c, best = s;
         }
@@ -1189,11 +1189,13 @@ Plan plan_of(const gdn_prefix_attn_desc *D) {
     p.own_tiles = p.own_warp ? 1 : (int)((per_seq + kRows - 1) / kRows);
     const int64_t prefix_base = (int64_t)D->num_kv_heads * p.prefix_tiles;
     const int64_t own_base = (int64_t)D->num_seqs * D->num_kv_heads * p.own_tiles;
-    // own keys beside the prefix, at half of the tables' room and 6.4 TB/s
-    const double own_us = (double)D->num_seqs * own_room * D->num_kv_heads * D->head_dim * 4 / 2 / 6.4e6 * kSms;
+    p.own_splits = !own_room ? 0 : p.own_warp ? warp_split(own_base, own_room) : tile_split(own_base, (own_room + kTile - 1) / kTile, 0.0);
+    // Own keys beside the prefix: half of the tables' room at 6.4 TB/s, but not above 1024 tokens a sequence (tables with
+    // room for more are mostly as wide as a sequence may ever get), and 1.7 SM-microseconds a CTA for its start and end.
+    const double own_us = (double)D->num_seqs * std::min<int64_t>(own_room / 2, 1024) * D->num_kv_heads * D->head_dim * 4 / 6.4e6 * kSms +
+                          1.7 * (double)(own_base * p.own_splits);
     p.prefix_splits = !D->prefix_len ? 0 : p.prefix_warp ? warp_split(prefix_base, D->prefix_len)
                                                          : tile_split(prefix_base, ((int64_t)D->prefix_len + kTile - 1) / kTile, own_us);
-    p.own_splits = !own_room ? 0 : p.own_warp ? warp_split(own_base, own_room) : tile_split(own_base, (own_room + kTile - 1) / kTile, 0.0);
     p.prefix_items = (int64_t)D->num_kv_heads * p.prefix_tiles * p.prefix_splits;
     p.own_items = (int64_t)D->num_seqs * D->num_kv_heads * p.own_tiles * p.own_splits;
     p.parts = p.prefix_splits + p.own_splits;
