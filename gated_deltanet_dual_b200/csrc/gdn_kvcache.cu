@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(THREADS) gdn_kv_extend_kernel(const __grid_con
     const int row0 = (int)min((int64_t)blockIdx.x * P.rows_per_cta, (int64_t)P.M);
     const int row1 = (int)min((int64_t)row0 + P.rows_per_cta, (int64_t)P.M);
     const int32_t count = *P.free_count;
-    const int64_t room = (int64_t)P.W * P.page;
+    const int64_t room = min((int64_t)P.W * P.page, (int64_t)INT32_MAX);     // lengths are int32
     bool bad = false;
     int64_t need_before = 0, new_before = 0;    // sums of the earlier passes
     if (tid == 0) s_taken = 0, s_count = 0;
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(THREADS) gdn_kv_extend_kernel(const __grid_con
             wrong[i] = len[i] < 0 || w[i] < 0 || (int64_t)len[i] + w[i] > room;
             w[i] = max(w[i], 0);
             my_new += w[i];
-            // up to 2^31 - 1 + page - 1 < 2^32
+            // lengths with their new tokens stay below 2^31 (room), pages too: sums below 2^32
             have[i] = wrong[i] ? 0 : (int)pages_in(P, (uint32_t)len[i] + (uint32_t)(P.page - 1));
             need[i] = wrong[i] ? 0 : (int)pages_in(P, (uint32_t)len[i] + (uint32_t)w[i] + (uint32_t)(P.page - 1)) - have[i];
             my_need += need[i];

@@ -60,8 +60,8 @@ typedef struct {
  * Outputs are apart from the inputs, so a call with the same inputs gives the same answer (and
  * writes the same table entries): feed seq_lens_out and free_left to the next step.
  * A sequence is refused (its rows get slot and position -1, its table row stays, its seq_lens_out is
- * its s, it takes no pages) when s or w is negative (w then counts as 0), its tokens would
- * pass W p or its rows M, or its pages do not fit: the pages that the sequences up to and with it
+ * its s, it takes no pages) when s or w is negative (w then counts as 0), its tokens s + w would
+ * pass W p or INT32_MAX or its rows M, or its pages do not fit: the pages that the sequences up to and with it
  * need (refused ones for the other reasons not counted) pass free_count.  device_status (optional,
  * may be NULL) is cleared, then set to GDN_ERR_INVALID_ARG if any was refused or free_count lies
  * outside [0, F] (it is clamped), or if a row falls on a page id that is negative or whose slot passes

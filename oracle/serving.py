@@ -61,7 +61,7 @@ def kv_extend(table, lens, new, free, count, page, rows, prefix_len=0):
     cu, out_lens, wanted, taken, at = [0], [], 0, 0, 0
     for n in range(n_seq):
         s, w = int(lens[n]), int(new[n])
-        refused = s < 0 or w < 0 or s + w > width * page
+        refused = s < 0 or w < 0 or s + w > min(width * page, 2 ** 31 - 1)
         w = max(w, 0)
         refused = refused or at + w > rows
         if not refused:

@@ -95,6 +95,24 @@ def test_sums_past_32_bits():
     assert int(status) == b.GDN_ERR_INVALID_ARG and int(table.count_nonzero()) == 1
 
 
+def test_lengths_near_the_last_int32():
+    """Tables with room for more tokens than an int32 length counts: refused past 2^31 - 1, served up to it."""
+    page, W = 1 << 20, 2049
+    table = np.arange(3 * W).reshape(3, W) % 2000
+    w = _check(table, [2**31 - 10, 2**31 - 10, 5], [20, 9, 2], [2001, 2002], 2, page, 34)
+    assert w["bad"] and list(w["lens"]) == [2**31 - 10, 2**31 - 1, 7] and w["left"] == 2
+    # pages of 2^31 - 1 tokens, the count of pages next to 2^32; the free list is empty
+    table = np.array([[0, 7, 7], [0, 7, 7], [0, 7, 7]])
+    w = _check(table, [2**31 - 1, 2**31 - 3, 2**31 - 1], [5, 2, 0], [], 0, 2**31 - 1, 8)
+    assert w["bad"] and list(w["lens"]) == [2**31 - 1] * 3 and np.array_equal(w["table"], table)
+    # positions saturate where the prefix takes them past the last int32
+    t = b.KvTables(1, 2)
+    b.kv_extend(_i32([[0] * W]), _i32([2**31 - 4]), _i32([2]), _i32([]), _i32([0]), page, t, prefix_len=2)
+    assert t.positions.tolist() == [2**31 - 2, 2**31 - 1] and t.seq_lens.tolist() == [2**31 - 2]
+    b.kv_extend(_i32([[0] * W]), _i32([2**31 - 4]), _i32([2]), _i32([]), _i32([0]), page, t, prefix_len=2**31 - 1)
+    assert t.positions.tolist() == [2**31 - 1] * 2
+
+
 def test_bad_page_ids_give_no_slot():
     t = b.KvTables(2, 2)
     status = _i32([0])

@@ -47,6 +47,13 @@ def test_frequency_scalings():
     assert np.all(ramp <= f + 1e-18) and np.all(ramp >= f / 4 - 1e-18)
 
 
+def test_lengths_stay_int32():
+    """A sequence's tokens do not pass 2^31 - 1, however much room its table has."""
+    table = np.zeros((2, 2049), int)
+    r = o.kv_extend(table, [2**31 - 10, 2**31 - 10], [10, 9], [], 0, 1 << 20, 19)
+    assert r["bad"] and list(r["lens"]) == [2**31 - 10, 2**31 - 1] and r["slot_map"][:10].tolist() == [-1] * 10
+
+
 def test_tables_keep_every_page_single():
     """Pages of all sequences stay distinct, slots of all tokens too, over several steps."""
     rng = np.random.default_rng(2)
