@@ -308,10 +308,12 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
     auto v_at = [&](int j) { return j + 1 < tiles ? 2 * j + 2 : 2 * j + 1; };
     const int box_rows = min(P.page, 64), boxes = kTile / box_rows, box = lane % boxes, half_of = lane / boxes;
     // This lane's cache row in key tile j, for K and again for V; the page ids of the tile after are on their way.
-    int id_next = -1, rows_of[2] = {0, 0};
+    int id_next = 0, rows_of[2] = {0, 0};
+    bool id_wanted = false;                    // any id may stand in the table: whether there is one is kept apart
     auto fetch_id = [&](int j) {
         const int key = (w.t0 + j) * kTile + box * box_rows;
-        id_next = half_of < kHalves && j < tiles && key < w.keys ? w.list[key / P.page] : -2;
+        id_wanted = half_of < kHalves && j < tiles && key < w.keys;
+        if (id_wanted) id_next = w.list[key / P.page];
     };
     auto load = [&](int i) {
         const bool value = i > 0 && ((i & 1) == 0 || i == 2 * tiles - 1);
@@ -320,8 +322,10 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
         if (!value) {
             const int id = id_next;
             int row = P.pages * P.page;        // past the end: reads as zeros
-            if (id >= 0 && id < P.pages) row = id * P.page + ((w.t0 + j) * kTile + box * box_rows) % P.page;
-            else if (id != -2) atomicOr(&s_status, (int)GDN_ERR_INVALID_ARG);
+            if (id_wanted) {
+                if (id >= 0 && id < P.pages) row = id * P.page + ((w.t0 + j) * kTile + box * box_rows) % P.page;
+                else atomicOr(&s_status, (int)GDN_ERR_INVALID_ARG);
+            }
             if (j & 1) rows_of[1] = row;
             else rows_of[0] = row;
             fetch_id(j + 1);

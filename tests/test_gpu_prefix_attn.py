@@ -200,6 +200,29 @@ def test_bad_lengths_and_pages_are_reported():
         assert torch.equal(out[1], _run(zero, True)[1])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,L,G,prefix", [(2, 1, 2, 70), (20, 1, 2, 300), (4, 17, 2, 300), (1, 40, 1, 0)])
+def test_every_bad_page_id_is_reported(N, L, G, prefix, d):
+    """Ids just outside the cache and far from it, in both tables, for few rows and for many, in the first key tile
+    and in a later one: reported, and read as zero keys and values."""
+    own = 200
+    p = _problem(N, L, 2 * G, 2, d, 16, prefix, [own] * N, seed=21)
+    ws, P = b.Workspace(1 << 24), p["k_cache"].shape[0]
+    places = [("block_table", (N - 1, 0)), ("block_table", (0, own // 16))]
+    places += [("prefix_pages", (0,)), ("prefix_pages", (prefix // 16,))] if prefix else []
+    for name, at in places:
+        page = int(p[name][at])
+        zero = dict(p, k_cache=p["k_cache"].clone(), v_cache=p["v_cache"].clone())
+        zero["k_cache"][page] = zero["v_cache"][page] = 0
+        want = _run(zero, False)
+        for bad in (-1, -2, -3, P, P + 1, 2**31 - 1, -2**31):
+            table = p[name].clone()
+            table[at] = bad
+            out = b.prefix_attention(**{**p, name: table}, causal=False, workspace=ws)
+            assert b.read_device_status(ws) == b.GDN_ERR_INVALID_ARG, (name, at, bad)
+            assert torch.equal(out, want), (name, at, bad)
+
+
 def test_same_bits_streams_and_graphs():
     p = _problem(20, 2, 8, 2, 128, 16, 900, [37] * 20, seed=11)
     want = _run(p, True)
