@@ -406,116 +406,117 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
     // V rows from key `newest` on are not for every query row (see the file comment): warp 19 cleans their tiles
     const int newest = (w.n >= 0 && P.causal) ? w.keys - (P.L - 1) : w.keys;
 
-    if (warp == 16) {
-        // ---------------------------------------------------------------- loads
+    // one instruction for all four warps of a warpgroup: those of the last take different roles behind it
+    if (warp >= 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-        int issued = min(kStages, 2 * tiles);
-        for (; issued < 2 * tiles; ++issued) {
-            wait(&empty[issued % kStages], (issued / kStages - 1) & 1, 1);
-            __syncwarp();
-            if (__any_sync(0xffffffffu, stopped())) break;     // the slot may still be in use
-            load(issued);
-        }
-        if (__any_sync(0xffffffffu, stopped()) && lane == 0)   // gave up: the loads in flight still land
-            for (int i = max(0, issued - kStages); i < issued; ++i)
-                mbar_wait(&full[i % kStages], (i / kStages) & 1, kDrainWaitIters);
-    } else if (warp == 17 || warp == 19) {
-        // ---------------------------------------------------------------- products: S (warp 17), P V (warp 19)
-        // Two streams, so that one's products run while the other waits on a barrier; warp-uniform, with few
-        // instructions between the products (a single thread's chain of address arithmetic and branches
-        // cost more than the products that it fed).
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-        constexpr uint32_t kStep = kTileBytes >> 4;
-        int slot = 0, left = tiles;
-        uint32_t phase = 0;
-        auto advance = [&](int n) {            // n tiles on in the ring
-            slot += n;
-            if (slot >= kStages) slot -= kStages, phase ^= 1;
-        };
-        if (warp == 17) {
-            constexpr uint32_t idesc = make_idesc_bf16(128, 128, 0, 0);
-            const uint64_t dq = make_sdesc(smem_u32(sm_q), 16, 1024), dk = make_sdesc(smem_u32(sm_kv), 16, 1024);
-            uint32_t odd = 0;                  // parity of the key tile
-            for (int j = 0; j < tiles; ++j, odd ^= 1) {
-                wait(&full[slot], phase, 2);
-                for (int t = 0; t <= two; ++t) {
-                    // the S before this one (of the other row tile, or of this one) is in registers
-                    if (t == 1) wait(&bar_r[0], odd, 3);
-                    else if (j > 0) wait(&bar_r[two], odd ^ 1, 3);
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
-                            mma_bf16(tb + T_S, dq + t * kStep + off, dk + slot * kStep + off, idesc, kk > 0);
-                        }
-                        mma_commit(&bar_s[t]);
-                        if (t == two) mma_commit(&empty[slot]);
-                    }
-                    __syncwarp();
-                }
-                advance(j == 0 ? 1 : 2);
-                if (__any_sync(0xffffffffu, stopped())) break;
+        if (warp == 16) {
+            // ---------------------------------------------------------------- loads
+            int issued = min(kStages, 2 * tiles);
+            for (; issued < 2 * tiles; ++issued) {
+                wait(&empty[issued % kStages], (issued / kStages - 1) & 1, 1);
+                __syncwarp();
+                if (__any_sync(0xffffffffu, stopped())) break;     // the slot may still be in use
+                load(issued);
             }
-        } else {
-            constexpr uint32_t idesc = make_idesc_bf16(128, D, 0, 1);
-            const uint64_t dv = make_sdesc(smem_u32(sm_kv), kTile * 128, 1024);
-            int end = (w.t0 + 1) * kTile;
-            slot = tiles > 1 ? 2 : 1;
-            for (int j = 0; j < tiles; ++j, end += kTile) {
-                wait(&full[slot], phase, 4);
-                if (end > newest) {
-                    const int key0 = end - kTile;
-                    uint8_t *v = sm_kv + slot * kTileBytes;
-                    const int last = min(kTile, w.keys - key0);          // rows [last, 128) are behind the list's end
-                    for (int i = lane; i < (kTile - last) * (D / 8); i += 32) {
-                        const int r = last + i / (D / 8), c = i % (D / 8);
-                        *reinterpret_cast<uint4 *>(v + (c >> 3) * (kTile * 128) + sw128_off(r, c & 7)) = make_uint4(0, 0, 0, 0);
-                    }
-                    const int lo = max(newest - key0, 0);                // rows [lo, last) are visible to some rows only
-                    bool found = false;
-                    for (int i = lane; i < (last - lo) * (D / 8); i += 32) {
-                        const int r = lo + i / (D / 8), c = i % (D / 8);
-                        uint32_t *p = reinterpret_cast<uint32_t *>(v + (c >> 3) * (kTile * 128) + sw128_off(r, c & 7));
+            if (__any_sync(0xffffffffu, stopped()) && lane == 0)   // gave up: the loads in flight still land
+                for (int i = max(0, issued - kStages); i < issued; ++i)
+                    mbar_wait(&full[i % kStages], (i / kStages) & 1, kDrainWaitIters);
+        } else if (warp == 17 || warp == 19) {
+            // ---------------------------------------------------------------- products: S (warp 17), P V (warp 19)
+            // Two streams, so that one's products run while the other waits on a barrier; warp-uniform, with few
+            // instructions between the products (a single thread's chain of address arithmetic and branches
+            // cost more than the products that it fed).
+            constexpr uint32_t kStep = kTileBytes >> 4;
+            int slot = 0, left = tiles;
+            uint32_t phase = 0;
+            auto advance = [&](int n) {            // n tiles on in the ring
+                slot += n;
+                if (slot >= kStages) slot -= kStages, phase ^= 1;
+            };
+            if (warp == 17) {
+                constexpr uint32_t idesc = make_idesc_bf16(128, 128, 0, 0);
+                const uint64_t dq = make_sdesc(smem_u32(sm_q), 16, 1024), dk = make_sdesc(smem_u32(sm_kv), 16, 1024);
+                uint32_t odd = 0;                  // parity of the key tile
+                for (int j = 0; j < tiles; ++j, odd ^= 1) {
+                    wait(&full[slot], phase, 2);
+                    for (int t = 0; t <= two; ++t) {
+                        // the S before this one (of the other row tile, or of this one) is in registers
+                        if (t == 1) wait(&bar_r[0], odd, 3);
+                        else if (j > 0) wait(&bar_r[two], odd ^ 1, 3);
+                        tc_fence_after();
+                        if (elect_one()) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t x = p[e];
-                            const bool a = (x & 0x7f80u) == 0x7f80u, b = (x & 0x7f800000u) == 0x7f800000u;
-                            if (a) x &= 0xffff0000u;
-                            if (b) x &= 0xffffu;
-                            if (a || b) {
-                                p[e] = x;
-                                found = true;
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t off = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
+                                mma_bf16(tb + T_S, dq + t * kStep + off, dk + slot * kStep + off, idesc, kk > 0);
+                            }
+                            mma_commit(&bar_s[t]);
+                            if (t == two) mma_commit(&empty[slot]);
+                        }
+                        __syncwarp();
+                    }
+                    advance(j == 0 ? 1 : 2);
+                    if (__any_sync(0xffffffffu, stopped())) break;
+                }
+            } else {
+                constexpr uint32_t idesc = make_idesc_bf16(128, D, 0, 1);
+                const uint64_t dv = make_sdesc(smem_u32(sm_kv), kTile * 128, 1024);
+                int end = (w.t0 + 1) * kTile;
+                slot = tiles > 1 ? 2 : 1;
+                for (int j = 0; j < tiles; ++j, end += kTile) {
+                    wait(&full[slot], phase, 4);
+                    if (end > newest) {
+                        const int key0 = end - kTile;
+                        uint8_t *v = sm_kv + slot * kTileBytes;
+                        const int last = min(kTile, w.keys - key0);          // rows [last, 128) are behind the list's end
+                        for (int i = lane; i < (kTile - last) * (D / 8); i += 32) {
+                            const int r = last + i / (D / 8), c = i % (D / 8);
+                            *reinterpret_cast<uint4 *>(v + (c >> 3) * (kTile * 128) + sw128_off(r, c & 7)) = make_uint4(0, 0, 0, 0);
+                        }
+                        const int lo = max(newest - key0, 0);                // rows [lo, last) are visible to some rows only
+                        bool found = false;
+                        for (int i = lane; i < (last - lo) * (D / 8); i += 32) {
+                            const int r = lo + i / (D / 8), c = i % (D / 8);
+                            uint32_t *p = reinterpret_cast<uint32_t *>(v + (c >> 3) * (kTile * 128) + sw128_off(r, c & 7));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t x = p[e];
+                                const bool a = (x & 0x7f80u) == 0x7f80u, b = (x & 0x7f800000u) == 0x7f800000u;
+                                if (a) x &= 0xffff0000u;
+                                if (b) x &= 0xffffu;
+                                if (a || b) {
+                                    p[e] = x;
+                                    found = true;
+                                }
                             }
                         }
+                        if (found) atomicOr(&s_status, kItemNonfinite);
+                        fence_async_smem();
+                        __syncwarp();
                     }
-                    if (found) atomicOr(&s_status, kItemNonfinite);
-                    fence_async_smem();
-                    __syncwarp();
-                }
-                for (int t = 0; t <= two; ++t) {
-                    wait(&bar_p[t], j & 1, 6);
-                    tc_fence_after();
-                    if (elect_one()) {
+                    for (int t = 0; t <= two; ++t) {
+                        wait(&bar_p[t], j & 1, 6);
+                        tc_fence_after();
+                        if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            mma_bf16_ts(tb + T_O + 128 * t, tb + T_P + 64 * t + kk * 8, dv + slot * kStep + kk * 128, idesc, j > 0 || kk > 0);
-                        mma_commit(&bar_o[t]);
-                        if (t == two) mma_commit(&empty[slot]);
+                            for (int kk = 0; kk < 8; ++kk)
+                                mma_bf16_ts(tb + T_O + 128 * t, tb + T_P + 64 * t + kk * 8, dv + slot * kStep + kk * 128, idesc,
+                                            j > 0 || kk > 0);
+                            mma_commit(&bar_o[t]);
+                            if (t == two) mma_commit(&empty[slot]);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    advance(--left > 1 ? 2 : 1);   // the last V follows the one before it
+                    if (__any_sync(0xffffffffu, stopped())) break;
                 }
-                advance(--left > 1 ? 2 : 1);   // the last V follows the one before it
-                if (__any_sync(0xffffffffu, stopped())) break;
             }
+            if (__any_sync(0xffffffffu, stopped()) && elect_one()) {       // gave up: the MMAs in flight still end
+                mma_commit(&bar_drain[warp == 19]);
+                mbar_wait(&bar_drain[warp == 19], 0, kDrainWaitIters);
+            }
+            __syncwarp();
         }
-        if (__any_sync(0xffffffffu, stopped()) && elect_one()) {       // gave up: the MMAs in flight still end
-            mma_commit(&bar_drain[warp == 19]);
-            mbar_wait(&bar_drain[warp == 19], 0, kDrainWaitIters);
-        }
-        __syncwarp();
-    } else if (warp > 16) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     } else {
         // ---------------------------------------------------------------- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));

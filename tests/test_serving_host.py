@@ -3,6 +3,7 @@ CPU only: placeholder addresses that the host validation must reject before anyt
 import copy
 import ctypes
 import math
+import os
 
 import numpy as np
 import pytest
@@ -243,6 +244,13 @@ def test_attention_refuses_overlaps(out, other, shift):
 @no_gpu
 def test_attention_refuses_a_scale_past_fp32():
     assert _call("gdn_prefix_attn", _with(ATT, scale=3e38), A[:8], ctypes.c_size_t(1 << 60), None) == 1
+
+
+def test_register_split_is_one_instruction_a_side():
+    """setmaxnreg must be the same instruction for all four warps of a warpgroup: one that takes and one that gives."""
+    with open(os.path.join(os.path.dirname(b.LIB_PATH), "csrc", "gdn_prefix_attn.cu")) as f:
+        source = f.read()
+    assert source.count("setmaxnreg.dec") == 1 and source.count("setmaxnreg.inc") == 1
 
 
 # ----------------------------------------------------------------------------- the Python layer
