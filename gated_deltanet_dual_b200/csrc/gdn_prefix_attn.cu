@@ -1085,6 +1085,9 @@ __global__ void __launch_bounds__(128) gdn_attn_combine_kernel(const __grid_cons
                 }
             }
         }
+    } else if (P.prefix > 0 || (P.causal ? s - (P.L - 1 - l) : s) > 0) {      // keys, but every score is -inf: 0 / 0
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] = NAN;
     }
     __nv_bfloat16 *out = P.out + row * D + lane * C;
     if constexpr (C == 4) *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf2(acc[0], acc[1]), pack_bf2(acc[2], acc[3]));

@@ -131,7 +131,7 @@ size_t gdn_prefix_attn_workspace_size(const gdn_prefix_attn_desc *desc);
 /* out[n, l, h] = softmax(scale q[n, l, h] . K) V over the Lp prefix keys and the first c own keys of
  * sequence n, key/value head h / (H / H_kv); c = seq_lens[n] when causal = 0 (the L tokens see one
  * another), else max(0, seq_lens[n] - (L - 1 - l)) (token l is the l-th of the L newest).  A row that
- * sees no key is 0.
+ * sees no key is 0; one whose scores are all -inf is NaN, as is one with a score of +inf or NaN.
  *   q, out [N, L, H, d] bf16 (neither out nor the workspace may overlap an input or one another:
  *   GDN_ERR_INVALID_ARG); workspace >= the size above, 256-byte
  *   aligned, contents on entry ignored; its first word is the status that

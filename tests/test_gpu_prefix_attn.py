@@ -177,6 +177,29 @@ def test_rows_that_see_nothing_are_zero():
     assert int(torch.count_nonzero(_run(empty, True))) == 0
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,L,G,prefix", [(2, 1, 2, 0), (2, 1, 2, 40), (3, 17, 1, 0), (20, 1, 2, 300), (2, 20, 2, 200)])
+def test_scores_without_bound(N, L, G, prefix, d):
+    """Scores of -inf and +inf, by infinite queries and keys: as softmax has them, for few rows and for many."""
+    own = 180
+    p = _problem(N, L, 2 * G, 2, d, 16, prefix, [own] * N, seed=22)
+    one = dict(p, q=p["q"].clone(), k_cache=p["k_cache"].clone())
+    one["k_cache"][..., 0] = 1.0
+    one["q"][0, 0, 0, 0], one["q"][N - 1, L - 1, G, 0] = -float("inf"), float("inf")
+    got = _run(one, True)
+    _close(got, _oracle(one, True), d)
+    assert torch.isnan(got[0, 0, 0]).all() and torch.isnan(got[N - 1, L - 1, G]).all()
+    some = dict(p, k_cache=p["k_cache"].clone(), q=p["q"].clone())             # one list of keys without bound
+    some["q"][..., 0] = 1.0
+    some["k_cache"][(p["prefix_pages"] if prefix else p["block_table"][0]).long(), :, 0, 0] = -float("inf")
+    want = _oracle(some, True)
+    _close(_run(some, True), want, d)
+    assert np.isnan(want[0]).any() == (prefix == 0)
+    if prefix:                                                                 # the own keys alone
+        none = dict(some, prefix_len=0)
+        assert torch.equal(_run(some, False)[:, :, :G], _run(none, False)[:, :, :G])
+
+
 def test_bad_lengths_and_pages_are_reported():
     p = _problem(4, 1, 2, 1, 128, 16, 40, [20, 30, 10, 5], seed=10)
     good = _run(p, True)
