@@ -144,3 +144,23 @@ def test_sizes_past_32_bits_are_refused():
     for page, prefix in (((1 << 32) + 16, 4), (16, (1 << 32) + 4), (16, -(1 << 32))):
         with pytest.raises(ValueError):
             run(page, prefix)
+
+
+def test_tables_past_32_bits_are_refused():
+    """Tensors whose sizes do not fit an int32 (17 GB, never written or read)."""
+    far = torch.empty((1 << 32) + 2, dtype=torch.int32, device="cuda")
+    args = dict(block_table=_i32([[-1, -1]]), seq_lens=_i32([0]), new_lens=_i32([3]), free_pages=_i32([7, 5]),
+                free_count=_i32([2]), page_size=16, tables=b.KvTables(1, 3))
+    for over in (dict(block_table=far.view(1, -1)), dict(free_pages=far)):
+        with pytest.raises(ValueError):
+            b.kv_extend(**args | over)
+    q, cache, few = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, 16, 1, 64, dtype=torch.bfloat16, device="cuda"), _i32([0])
+    rows = q.expand(1 << 32, 1, 64)
+    with pytest.raises(ValueError):                         # 2^32 rows are not none
+        b.rotary_append(rows, rows, rows, far[:1 << 32], far[:1 << 32], b.rotary_table(64), cache, cache.clone(), q_out=rows)
+    with pytest.raises(ValueError):
+        b.rotary_forward(rows, None, far[:1 << 32], b.rotary_table(64), q_out=rows)
+    for over in (dict(block_table=far.view(1, -1)), dict(prefix_pages=far, prefix_len=(1 << 32) + 5)):
+        with pytest.raises(ValueError):
+            b.prefix_attention(**dict(q=q.view(1, 1, 1, 64), k_cache=cache, v_cache=cache, prefix_pages=None, prefix_len=0,
+                                      block_table=_i32([[0]]), seq_lens=few) | over)
