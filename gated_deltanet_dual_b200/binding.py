@@ -737,6 +737,8 @@ class RotaryTable:
     def _on(self, index: int):
         if self._index != index:
             raise ValueError(f"the rotary table is on {self._turns.device}, expected cuda:{index}")
+        if self._turns.data_ptr() != self._ptr:
+            raise ValueError("the rotary table's tensor was resized or replaced")
         return self._ptr
 
 
@@ -824,7 +826,14 @@ class KvTables:
         self._tensors = tuple(torch.empty(n, dtype=torch.int32, device=device) for n in sizes)
         self._index = self._tensors[4].get_device()
         self._sizes = int(num_seqs), int(max_new_tokens)
-        self._ptrs = tuple(t.data_ptr() if t.numel() else None for t in self._tensors)
+        self._ptrs = tuple(t.data_ptr() for t in self._tensors)
+
+    def _where(self):
+        """The tensors' addresses (0 where there are no rows); their memory is still that of the sizes they were made for."""
+        a, b, c, d, e = self._tensors
+        if (a.data_ptr(), b.data_ptr(), c.data_ptr(), d.data_ptr(), e.data_ptr()) != self._ptrs:
+            raise ValueError("a tensor of the tables was resized or replaced")
+        return self._ptrs
 
     slot_map = property(lambda self: self._tensors[0])
     positions = property(lambda self: self._tensors[1])
@@ -860,7 +869,7 @@ def kv_extend(block_table, seq_lens, new_lens, free_pages, free_count, page_size
         _int32(page_size=page_size, prefix_len=prefix_len, num_seqs=N, table_width=W, num_free=F, max_new_tokens=M)
     desc = KvExtendDesc(N, W, page_size, F, M, prefix_len, 0, 0)
     _call("gdn_kv_extend", index, stream, ctypes.byref(desc), block_table.data_ptr(), seq_lens.data_ptr(),
-          new_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), *tables._ptrs,
+          new_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), *tables._where(),
           None if device_status is None else device_status.data_ptr())
     return tables
 

@@ -164,3 +164,15 @@ def test_tables_past_32_bits_are_refused():
         with pytest.raises(ValueError):
             b.prefix_attention(**dict(q=q.view(1, 1, 1, 64), k_cache=cache, v_cache=cache, prefix_pages=None, prefix_len=0,
                                       block_table=_i32([[0]]), seq_lens=few) | over)
+
+
+def test_tables_that_were_resized():
+    t = b.KvTables(1, 3)
+    args = (_i32([[-1, -1]]), _i32([0]), _i32([3]), _i32([7, 5]), _i32([2]), 16, t)
+    b.kv_extend(*args)
+    t.slot_map.resize_(1 << 20)
+    with pytest.raises(ValueError):
+        b.kv_extend(*args)
+    none = b.KvTables(1, 0)                                  # no rows: nothing to move
+    b.kv_extend(_i32([[-1]]), _i32([0]), _i32([0]), _i32([]), _i32([0]), 16, none)
+    assert none.cu_new.tolist() == [0, 0]

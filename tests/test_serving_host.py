@@ -270,6 +270,32 @@ def test_python_layer_wants_cuda_tensors():
         b.rotary_forward(None, None, i(2), t)
 
 
+def test_tables_that_moved_are_refused():
+    """Memory that a caller has taken from a table's tensors is not written or read."""
+    make = lambda: b.KvTables(2, 4, "cpu")
+    assert len(make()._where()) == 5 and b.KvTables(2, 0, "cpu")._where()[:2] == (0, 0)
+    for name in ("slot_map", "positions", "cu_new", "seq_lens", "free_left"):
+        t = make()
+        getattr(t, name).fill_(3)                           # its contents are the caller's
+        t._where()
+        getattr(t, name).resize_(1 << 20)
+        with pytest.raises(ValueError):
+            t._where()
+        t = make()
+        getattr(t, name).data = torch.zeros(5, dtype=torch.int32)
+        with pytest.raises(ValueError):
+            t._where()
+        t = make()
+        getattr(t, name).untyped_storage().resize_(0)
+        with pytest.raises(ValueError):
+            t._where()
+    r = b.RotaryTable(torch.zeros(4, dtype=torch.int64), 8, False, 1.0)
+    r._on(-1)
+    r.turns.resize_(1 << 20)
+    with pytest.raises(ValueError):
+        r._on(-1)
+
+
 def test_python_layer_refuses_what_32_bits_do_not_hold():
     for rot in (1 << 32, (1 << 32) + 64, -(1 << 32)):
         with pytest.raises(ValueError):
