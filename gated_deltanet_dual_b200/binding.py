@@ -683,7 +683,7 @@ def _cuda_index(t: torch.Tensor) -> int:
     return index
 
 
-_PAST = 1 << 31                 # a size from here on does not fit the descriptors' int32
+_PAST = 1 << 31                 # a size from here on does not fit the descriptors' int32; so for their bits together
 
 
 def _int32(**values):
@@ -795,7 +795,7 @@ def _rotary(name, q, k, positions, table, q_out, k_out, stream):
         k_out = _fresh(k, k_shape, stream)
     _want(positions, "positions", (T,), torch.int32, index)
     turns = table._on(index)
-    if max(rows, H, Hkv, d) >= _PAST:
+    if rows | H | Hkv | d >= _PAST:
         _int32(rows=rows, num_heads=H, num_kv_heads=Hkv, head_dim=d)
     if rows and H + Hkv:
         desc = RotaryDesc(rows, T, H, Hkv, d, table._args[0], table._args[1], _dtype_code(lead), table._args[2], 0, *strides)
@@ -865,7 +865,7 @@ def kv_extend(block_table, seq_lens, new_lens, free_pages, free_count, page_size
         raise ValueError(f"tables are made for {tables._sizes[0]} sequences on {tables.free_left.device}, not for {N} on cuda:{index}")
     if device_status is not None:
         _want(device_status, "device_status", (1,), i32, index)
-    if not (0 < page_size < _PAST and 0 <= prefix_len < _PAST and max(N, W, F, M) < _PAST):
+    if not 0 <= page_size | prefix_len | N | W | F | M < _PAST:
         _int32(page_size=page_size, prefix_len=prefix_len, num_seqs=N, table_width=W, num_free=F, max_new_tokens=M)
     desc = KvExtendDesc(N, W, page_size, F, M, prefix_len, 0, 0)
     _call("gdn_kv_extend", index, stream, ctypes.byref(desc), block_table.data_ptr(), seq_lens.data_ptr(),
@@ -884,7 +884,7 @@ def rotary_append(q, k, v, positions, slot_map, table: RotaryTable, k_cache, v_c
         raise ValueError("q, k, v and q_out must be [R, heads, d] and the caches [P, p, H_kv, d]")
     R, H, d = q.shape
     Hkv, (P, page) = k.shape[1], k_cache.shape[:2]
-    if max(R, H, Hkv, d, P, page) >= _PAST:
+    if R | H | Hkv | d | P | page >= _PAST:
         _int32(num_rows=R, num_heads=H, num_kv_heads=Hkv, head_dim=d, num_pages=P, page_size=page)
     if q_out is None:
         q_out = _fresh(q, (R, H, d), stream)
@@ -958,7 +958,7 @@ def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len, block_table,
         _want(prefix_pages, "prefix_pages", (prefix_pages.numel(),), torch.int32, index)
         if prefix_len < 0 or prefix_pages.numel() < -(-prefix_len // page):
             raise ValueError(f"prefix_pages holds {prefix_pages.numel()} pages of {page} for {prefix_len} tokens")
-    if max(N, L, H, Hkv, d, page, P, W, prefix_len) >= _PAST:
+    if N | L | H | Hkv | d | page | P | W | prefix_len >= _PAST:
         _int32(num_seqs=N, num_tokens=L, num_heads=H, num_kv_heads=Hkv, head_dim=d, page_size=page, num_pages=P,
                table_width=W, prefix_len=prefix_len)
     if out is None:
