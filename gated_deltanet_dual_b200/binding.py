@@ -671,6 +671,8 @@ def _rows(t: Optional[torch.Tensor], name: str, shape, dtype, index: int):
         raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
+    if len(shape) == 4 and shape[1] == 1:      # a row a view: the views are the rows
+        return st[0], st[2]
     if len(shape) == 4 and shape[0] > 1 and st[0] != shape[1] * st[1]:
         raise ValueError(f"{name}: the views must lie {shape[1]} rows apart")
     return st[-3], st[-2]

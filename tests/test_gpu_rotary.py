@@ -244,3 +244,17 @@ def test_slices_of_one_buffer_in_place_and_beside():
     assert torch.equal(q, want[0]) and torch.equal(k, want[1])
     with pytest.raises(b.GdnError):
         b.rotary_forward(q, k, pos, table, q_out=buf[:, 1:5], k_out=ko)
+
+
+def test_one_position_of_many_views():
+    """A slice of one position: its views lie as far apart as the whole tensor's."""
+    table, f = _table(32, False, "none", 1.0)
+    x, out = _normal(_gen(8), 5, 7, 4, 64, dtype=torch.bfloat16), torch.zeros(5, 7, 2, 64, dtype=torch.bfloat16, device="cuda")
+    pos = torch.tensor([3], dtype=torch.int32, device="cuda")
+    q, k = x[:, 3:4, :2], x[:, 3:4, 2:]
+    qo, ko = b.rotary_forward(q, k, pos, table, k_out=out[:, 6:])
+    _close(qo, q, o.rotate(q, pos, f), f, False, 1.0, "q")
+    _close(ko, k, o.rotate(k, pos, f), f, False, 1.0, "k")
+    assert ko.data_ptr() == out[:, 6:].data_ptr() and int(out[:, :6].count_nonzero()) == 0
+    with pytest.raises(ValueError):                          # two positions of every view: no single row stride
+        b.rotary_forward(x[:, 3:5], None, torch.tensor([3, 4], dtype=torch.int32, device="cuda"), table)
