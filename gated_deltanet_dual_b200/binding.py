@@ -928,13 +928,15 @@ def prefix_attn_workspace_size(desc: PrefixAttnDesc) -> int:
 
 
 def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len, block_table, seq_lens, *, causal=True, scale=None,
-                     out=None, workspace: Optional[Workspace] = None, stream=None):
+                     out=None, workspace: Optional[Workspace] = None, device_status=None, stream=None):
     """Attention of the L newest tokens of N sequences, q [N, L, H, d] bf16, over a shared prefix (the
     first prefix_len tokens on the pages prefix_pages) and each sequence's own seq_lens[n] keys through
     block_table [N, W], in caches [P, p, H_kv, d] (gdn_prefix_attn).  causal=False lets the L tokens see
     one another (a denoised block).  scale None is 1 / sqrt(d).  A workspace (Workspace, of
-    prefix_attn_workspace_size bytes) belongs to one call at a time; None allocates one.  Returns out
-    [N, L, H, d]."""
+    prefix_attn_workspace_size bytes) belongs to one call at a time; None allocates one.  What is found wrong on the
+    device (a length or page id out of range, a wait that gave up) is in device_status [1] int32 once the call is
+    done, and in the workspace; the rows of a length out of range stay as they were, in a new out unset.  Returns
+    out [N, L, H, d]."""
     index, io = _cuda_index(q), q.dtype
     if q.ndim != 4 or k_cache.ndim != 4 or block_table.ndim != 2:
         raise ValueError("q must be [N, L, H, d], the caches [P, p, H_kv, d] and block_table [N, W]")
@@ -967,6 +969,12 @@ def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len, block_table,
         out = _fresh(q, shape, stream)
     else:
         _want(out, "out", shape, io, index)
+    if device_status is not None:
+        _want(device_status, "device_status", (1,), i32, index)
+        at = device_status.data_ptr()
+        for t in (q, k_cache, v_cache, prefix_pages, block_table, seq_lens, out, workspace and workspace.tensor):
+            if t is not None and t.data_ptr() < at + 4 and at < t.data_ptr() + t.numel() * t.element_size():
+                raise ValueError("device_status overlaps another tensor of the call")
     desc = PrefixAttnDesc(N, L, H, Hkv, d, page, P, W, prefix_len, 1 if causal else 0, _dtype_code(q),
                           0.0 if scale is None else scale)
     if workspace is None:
@@ -978,6 +986,13 @@ def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len, block_table,
     _call("gdn_prefix_attn", index, stream, ctypes.byref(desc), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           prefix_pages.data_ptr() if prefix_len else None, block_table.data_ptr() if W else None, seq_lens.data_ptr(),
           out.data_ptr(), ws.data_ptr(), ws.numel())
+    if device_status is not None:              # behind the call, on its stream
+        found = ws[:4].view(i32)
+        if stream is None:
+            device_status.copy_(found)
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=index)):
+                device_status.copy_(found)
     return out
 
 

@@ -223,6 +223,40 @@ def test_bad_lengths_and_pages_are_reported():
         assert torch.equal(out[1], _run(zero, True)[1])
 
 
+def test_device_status():
+    """What is found wrong on the device reaches a caller who keeps no workspace; on other streams and in graphs too."""
+    p = _problem(4, 1, 2, 1, 128, 16, 40, [20, 30, 10, 5], seed=10)
+    want, status = _run(p, True), _i32([55])
+    assert torch.equal(b.prefix_attention(**p, device_status=status), want) and int(status) == b.GDN_OK
+    bad = dict(p, seq_lens=_i32([20, -1, 33, 5]))
+    b.prefix_attention(**bad, device_status=status)
+    assert int(status) == b.GDN_ERR_INVALID_ARG
+    b.prefix_attention(**p, workspace=b.Workspace(1 << 22), device_status=status)
+    assert int(status) == b.GDN_OK
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    b.prefix_attention(**bad, device_status=status, stream=side.cuda_stream)
+    side.synchronize()
+    assert int(status) == b.GDN_ERR_INVALID_ARG
+    g, lens = torch.cuda.CUDAGraph(), p["seq_lens"].clone()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        out = b.prefix_attention(**dict(p, seq_lens=lens), device_status=status)
+    for now, code in ((p["seq_lens"], b.GDN_OK), (bad["seq_lens"], b.GDN_ERR_INVALID_ARG), (p["seq_lens"], b.GDN_OK)):
+        lens.copy_(now)
+        status.fill_(55)
+        g.replay()
+        assert int(status) == code
+    assert torch.equal(out, want)
+    for wrong in (_i32([0, 0]), torch.zeros(1, device="cuda"), torch.zeros(1, dtype=torch.int32)):
+        with pytest.raises((ValueError, TypeError)):
+            b.prefix_attention(**p, device_status=wrong)
+    with pytest.raises(ValueError):
+        b.prefix_attention(**p, device_status=p["seq_lens"][1:2])
+    with pytest.raises(ValueError):
+        b.prefix_attention(**p, out=torch.empty_like(want), device_status=p["q"].view(-1).view(torch.int32)[:1])
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("N,L,G,prefix", [(2, 1, 2, 70), (20, 1, 2, 300), (4, 17, 2, 300), (1, 40, 1, 0)])
 def test_every_bad_page_id_is_reported(N, L, G, prefix, d):
