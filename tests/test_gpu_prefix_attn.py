@@ -513,3 +513,90 @@ def test_tables_far_wider_than_the_lengths(N, L, H, Hkv, d, page):
     lens = np.random.default_rng(N).integers(0, 90, N).tolist()
     p = _problem(N, L, H, Hkv, d, page, 3000, lens, W=4000, seed=20)
     _close(_run(p, True), _oracle(p, True), d)
+
+
+def _newest(p, n, back):
+    """(page, offset) of the token `back` places before the last of sequence n."""
+    i, page = int(p["seq_lens"][n]) - 1 - back, p["k_cache"].shape[1]
+    return int(p["block_table"][n, i // page]), i % page
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("N,L,H,Hkv,d,page,prefix,most", [
+    (38, 17, 4, 4, 64, 16, 0, 1400),        # 152 CTAs of own keys, up to 11 key tiles each: two turns of the ring
+    (13, 20, 12, 12, 128, 64, 0, 1300),     # 156 CTAs
+    (3, 33, 8, 1, 128, 256, 300, 2000),     # 264 rows of a sequence: two CTAs a list, split
+    (2, 160, 2, 1, 64, 32, 100, 900),       # 320 rows; the newest tokens cover more than one key tile
+])
+def test_long_own_keys_of_many_rows(N, L, H, Hkv, d, page, prefix, most, causal):
+    """Own keys by the kernel of many rows, over many key tiles: lengths of their own, keys that grow along the list (the
+    reference max moves in later tiles), values that only some rows see."""
+    rng = np.random.default_rng(N)
+    lens = rng.integers(L, most, N)
+    lens[0], lens[-1] = most, L + 3
+    p = _problem(N, L, H, Hkv, d, page, prefix, lens.tolist(), seed=23)
+    grow = torch.ones(p["k_cache"].shape[:2], device="cuda")
+    for n, s in enumerate(lens.tolist()):
+        i = torch.arange(s, device="cuda")
+        grow[p["block_table"][n].long()[i // page], i % page] = 0.1 + 6.0 * i / s
+    p["k_cache"] = (p["k_cache"] * grow[..., None, None]).bfloat16()
+    _close(_run(p, causal), _oracle(p, causal), d)
+    if causal:
+        for n, back, c, x in ((0, 0, 3, float("inf")), (0, L - 2, 5, -float("inf")), (N - 1, 1, 0, float("nan"))):
+            pg, off = _newest(p, n, back)
+            p["v_cache"][pg, off, 0, c] = x
+        _close(_run(p, causal), _oracle(p, causal), d)
+
+
+@pytest.mark.parametrize("N,L,H,Hkv,d,page", [(3, 20, 4, 4, 128, 64), (2, 40, 4, 1, 64, 16), (150, 17, 1, 1, 64, 16)])
+def test_wide_tables_of_many_rows(N, L, H, Hkv, d, page):
+    lens = np.random.default_rng(N).integers(0, 400, N).tolist()
+    lens[0] = 0
+    p = _problem(N, L, H, Hkv, d, page, 200, lens, W=4000, seed=24)
+    _close(_run(p, True), _oracle(p, True), d)
+
+
+def test_a_mixed_step_as_it_is_served():
+    """Steps of decode rows and prompt chunks of unequal lengths: kv_extend packs them, rotary_append writes the cache, and
+    the queries go to prefix_attention behind padding on the left (token l is the l-th of the L newest)."""
+    rng, page, H, Hkv, d, Lp = np.random.default_rng(31), 16, 4, 2, 64, 37
+    g = torch.Generator(device="cuda")
+    g.manual_seed(31)
+    normal = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+    table, f = b.rotary_table(d), o.frequencies(d)
+    N, P, W = 4, 120, 24
+    kc, vc = normal(P, page, Hkv, d), normal(P, page, Hkv, d)
+    prefix_pages = _i32([9, 4, 30])
+    slots = prefix_pages.long().repeat_interleave(page)[:Lp] * page + torch.arange(Lp, device="cuda") % page
+    q, k, v = normal(Lp, H, d), normal(Lp, Hkv, d), normal(Lp, Hkv, d)
+    b.rotary_append(q, k, v, torch.arange(Lp, device="cuda", dtype=torch.int32), slots.int(), table, kc, vc)
+    free = _i32([p for p in rng.permutation(P) if p not in (9, 4, 30)])
+    bt, lens, left = _i32(np.full((N, W), -1)), _i32([0] * N), _i32([P - 3])
+    status = _i32([0])
+    for new in ([150, 1, 40, 0], [1, 1, 1, 1], [33, 0, 200, 7], [1, 17, 1, 1]):
+        t, M, L = b.KvTables(N, sum(new) + 5), sum(new), max(new)
+        b.kv_extend(bt, lens, _i32(new), free, left, page, t, prefix_len=Lp, device_status=status)
+        assert int(status) == b.GDN_OK
+        q, k, v = normal(M + 5, H, d), normal(M + 5, Hkv, d), normal(M + 5, Hkv, d)
+        q_rot = b.rotary_append(q, k, v, t.positions, t.slot_map, table, kc, vc, device_status=status)
+        assert int(status) == b.GDN_OK
+        padded, cu = normal(N, L, H, d), t.cu_new.tolist()
+        for n in range(N):
+            padded[n, L - new[n]:] = q_rot[cu[n]:cu[n + 1]]
+        out = b.prefix_attention(padded, kc, vc, prefix_pages, Lp, bt, t.seq_lens, device_status=status)
+        assert int(status) == b.GDN_OK
+        # against the oracle's own tables, positions and rotation; the cache's keys are bf16 there and here
+        want = o.prefix_attention(padded, kc, vc, prefix_pages, Lp, bt, t.seq_lens, causal=True)
+        _close(out, want, d)
+        for n in range(N):
+            pos = Lp + o.ints(lens)[n] + np.arange(new[n])
+            assert np.array_equal(o.ints(t.positions)[cu[n]:cu[n + 1]], pos)
+            i = o.ints(lens)[n] + np.arange(new[n])
+            at = o.ints(bt)[n][i // page], i % page
+            assert np.array_equal(o.f64(vc)[at], o.f64(v[cu[n]:cu[n + 1]]))
+            ref = o.rotate(k[cu[n]:cu[n + 1]], pos, f)
+            # the rounding to bf16, 2^-8 of the value, and the rotation's own 4e-7 (|x1| + |x2|), at most 8e-7 of the largest
+            near = np.abs(o.f64(k[cu[n]:cu[n + 1]])).max() if new[n] else 0.0
+            assert np.all(np.abs(o.f64(kc)[at] - ref) <= 2.0 ** -8 * np.abs(ref) + 8e-7 * near)
+        lens, left = t.seq_lens, t.free_left
+    assert o.ints(lens).tolist() == [185, 19, 242, 9]
