@@ -16,9 +16,9 @@
 // A and B.  A row (TMEM lane) has two threads, each with 64 of a tile's 128 scores: they share the maximum only
 // when it moves.  S_A and S_B take turns in the same TMEM columns, which are free as soon as the scores are in
 // registers; P (bf16) has columns of its own per row tile, so S(next) runs while this tile's exponentials
-// do.  Bound by the exponential unit and the shared memory reads of the products together: 256 requests of 4
-// query heads per key/value head over 16384 prefix keys take 74 us where the products alone are 40 us of the tensor
-// pipe's measured rate and the exponentials 30 us.
+// do.  In its loop bound by the tensor pipe: a tile step of 256 rows takes 1.6 us, of which the products take 1.45 at the
+// pipe's measured rate.  256 requests of 4 query heads per key/value head over 16384 prefix keys take 74 us: 44 of tile
+// steps on all SMs (the products 40), the rest a CTA's start and end (12 us) and the uneven last wave.
 //
 // gdn_warp_attn_kernel -- few query rows of a key list (L (H / H_kv) <= 16: a decode step): bound by
 // reading K and V, and a 128-row tile would be padding.  One CTA = (key list, key/value head, split),
@@ -62,7 +62,8 @@ constexpr int kRows = 2 * kTile;               // rows of a CTA
 constexpr int kStages = 5;                     // K and V tiles in flight
 constexpr int kTThreads = 640;                 // 16 softmax warps, load, S, idle, P V (register shares go by four warps)
 // Registers a thread: the launch gives 96 (65536 / 640, in eights); the softmax warps hold half a row of
-// S and take what the load and MMA warps give up.
+// S and take what the load and MMA warps give up.  The compiler spills 32 bytes a thread at d = 128 (24 at 64; 14 and
+// 12 stores of 4 bytes, 36 and 26 loads, in all roles together).
 constexpr int kRegsLaunch = 96, kRegsSoftmax = 104, kRegsOther = 56;
 static_assert(4 * kRegsSoftmax + kRegsOther <= 5 * kRegsLaunch, "a warpgroup would wait for registers for ever");
 constexpr int kWKeys = 64;                     // gdn_warp_attn_kernel: keys of a tile (16 per warp)
@@ -303,9 +304,16 @@ gdn_tile_attn_kernel(const __grid_constant__ PrefixParams P, const __grid_consta
     }
     const int two = w.nrows > kTile;           // row tile B is in use
 
-    // The ring's order is the order of use: K0 K1 V0 K2 V1 ... V(last).  Loads tile i of the ring (warp 16):
-    // lane = (half, box), a box is min(p, 64) rows of one page, 64 columns; rows past the end read as zeros.
-    auto v_at = [&](int j) { return j + 1 < tiles ? 2 * j + 2 : 2 * j + 1; };
+    // The ring's order is the order of use, K0 K1 V0 K2 V1 ... V(last): K(j) has place 2 j - 1 (K0: 0), V(j) 2 j + 2, the
+    // last V 2 tiles - 1.  Warp 17 waits for the K tiles and warp 19 for the V tiles, each by parity, which is right only
+    // if the slot's use before, kStages places back, has landed.  It has:
+    //   at K(j), warp 17 has seen S(j - 2) taken into registers, which the softmax warps do once P V(j - 4) is done: K(j - 1)
+    //   and V(j - 4) have landed, places 2 j - 3 and 2 j - 6, and what lies before each of the same kind;
+    //   at V(j), warp 19 has seen P(j - 1) written: V(j - 1) and K(j - 1), places 2 j and 2 j - 3, and so on.
+    // Four places or more back all is covered, at three it would not be.
+    static_assert(kStages >= 4, "a wait for a slot's use could pass on the parity of the use before the last");
+    // Loads tile i of the ring (warp 16): lane = (half, box), a box is min(p, 64) rows of one page, 64 columns; rows past
+    // the end read as zeros.
     const int box_rows = min(P.page, 64), boxes = kTile / box_rows, box = lane % boxes, half_of = lane / boxes;
     // This lane's cache row in key tile j, for K and again for V; the page ids of the tile after are on their way.
     int id_next = 0, rows_of[2] = {0, 0};
@@ -690,9 +698,9 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Tiles on their way: at d = 128 three CTAs an SM of two tiles (64 KB each, at most 136 registers a thread) beat two CTAs of
-// three, because one CTA's start lies behind two others' loads (own keys of 64 requests of up to 1024
-// tokens, 32 query heads on 8, 35 against 40 us; of 32 requests with 4 tokens each, 47 against 61 us, both with
+// Tiles on their way: at d = 128 three CTAs an SM of two tiles (64 KB each, at most 136 registers a thread, of which 16 rows
+// spill 16 bytes) beat two CTAs of three, because one CTA's start lies behind two others' loads (own keys of 64 requests of
+// up to 1024 tokens, 32 query heads on 8, 35 against 40 us; of 32 requests with 4 tokens each, 47 against 61 us, both with
 // the splits of that time; with the present ones 33 and 41 us).  One set of CTAs that stay and take one item after the
 // other without a gap in the loads was slower (37 and 55 us): the gaps of one CTA lie behind the others anyway.
 template <int D, int NT>

@@ -236,7 +236,8 @@ cudaError_t launch_rotary(const RotaryParams &P, bool vec, cudaStream_t st) {
 template <bool APPEND>
 gdn_status run_rotary(RotaryParams &P, int dtype, int interleaved, bool vec, cudaStream_t st) {
     // Rows per CTA: one up to 16 CTAs a SM (a decode step wants every SM), else as many as keep to that number, four
-    // waves, so that they share a CTA's set-up.  Append of 8192 rows: 3 rows (4.6 waves) 37.9 us, 4 rows 36.0, 1 row 45.8.
+    // waves, so that they share a CTA's set-up; never more than kRMaxRows, for which shared memory has room, so
+    // above 18944 rows the CTAs grow in number again (32768 rows: 28 a SM).  Append of 8192 rows: 3 rows (4.6 waves) 37.9 us, 4 rows 36.0, 1 row 45.8.
     P.rows_per_cta = (int)std::min<int64_t>(kRMaxRows, (P.rows + INT64_C(148) * 16 - 1) / (148 * 16));
     cudaError_t e;
     if (dtype == GDN_BF16)

@@ -96,7 +96,7 @@ typedef struct {
  * v_cache[s] = v[r].  Rows with slot -1 are padding: nothing of theirs is read or written.  A slot
  * below -1 or not below p P is skipped in the same way and sets device_status (optional; cleared by the
  * call) to GDN_ERR_INVALID_ARG.  Rows that share a slot race: a slot
- * belongs in slot_map once.  q_out may be q (same strides); every other overlap of an output (q_out, the
+ * belongs in slot_map once.  The caches have the rows' dtype; gdn_prefix_attn reads bf16 caches.  q_out may be q (same strides); every other overlap of an output (q_out, the
  * caches, device_status) with an input or another output is GDN_ERR_INVALID_ARG, where tensors count as
  * apart as gdn_rotary.h defines it. */
 gdn_status gdn_rotary_append(const gdn_append_desc *desc, const uint64_t *turns, const int32_t *positions,

@@ -17,8 +17,9 @@
  *                    0, 1): f_i (w + (1 - w) / factor); fast pairs keep f_i, slow ones are interpolated
  * A table stores each frequency as a fraction of a turn per position in 64-bit fixed point,
  * round(f_i / (2 pi) 2^64) mod 2^64.  The angle of position p is then p times that, modulo 2^64: whole
- * turns drop out exactly, and the error of the angle stays below 2^-30 turns at every int32 position
- * (a table entry is off by less than 2^-62 turns): far positions lose nothing.
+ * turns drop out exactly, and that angle is off by less than 2^-30 turns at every int32 position (a
+ * table entry by less than 2^-62 turns): far positions lose nothing.  For the sine and cosine the angle,
+ * less than half a turn, is rounded to fp32: another 2^-26 turns (9.4e-8 radians) at most.
  *
  * Layouts: rows of heads with the elements of a head contiguous; row and head strides in
  * ELEMENTS are the caller's (so q and k may be slices of one projection's output).
