@@ -1156,7 +1156,8 @@ struct Plan {
 
 // Splits of `tiles` key tiles over `base` equal lists for gdn_tile_attn_kernel, beside other work of `beside`
 // SM-microseconds in the same call.  A CTA has an SM to itself and takes kTileUs a key tile and kStartUs for its start and
-// end (measured at two row tiles, d = 128); the call takes as long as its waves of CTAs, or as all its work on all
+// end (measured at two row tiles, d = 128; taken for d = 64 and for one row tile too, where a tile is about half and
+// a quarter of that work); the call takes as long as its waves of CTAs, or as all its work on all
 // SMs, and each part a little in the combine step.  With own keys beside it a prefix is thus cut into fewer
 // parts than would fill the GPU: 16384 keys for 256 requests of up to 1024 own tokens, 3 parts of 32 CTAs
 // 108 us, 4 parts 122 us (2 parts 131 us); the prefix alone, 92 us and 74 us.
