@@ -1159,7 +1159,7 @@ struct Plan {
 // end (measured at two row tiles, d = 128; taken for d = 64 and for one row tile too, where a tile is about half and
 // a quarter of that work); the call takes as long as its waves of CTAs, or as all its work on all
 // SMs, and each part a little in the combine step.  With own keys beside it a prefix is thus cut into fewer
-// parts than would fill the GPU: 16384 keys for 256 requests of up to 1024 own tokens, 3 parts of 32 CTAs
+// parts than would fill the GPU: 16384 keys for 256 requests of up to 512 own tokens, 3 parts of 32 CTAs
 // 108 us, 4 parts 122 us (2 parts 131 us); the prefix alone, 92 us and 74 us.
 // The host knows the tables' room, not the lengths, so the prefix's own time may grow by a third and 6.5 us at the most: 64
 // requests of up to 1024 own tokens over 8192 prefix keys take 45 us with tables of that room (6 parts; 5 parts 48 us,
